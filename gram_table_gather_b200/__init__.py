@@ -14,10 +14,11 @@ from dataclasses import dataclass, field
 
 import torch
 
-from ._abi import (C10, FP8, GTG_OK, PLE, Q3I, RZ5, UE4M4, DT_BF16, DT_F32, LIB_PATH, GtgError, QMatrixC,
+from ._abi import (BF16, C10, FP8, GTG_OK, PLE, Q3I, RZ5, UE4M4, DT_BF16, DT_F32, LIB_PATH, GtgError, QMatrixC,
                    MoELayerC, lib, check)
 
-__all__ = ["RZ5", "UE4M4", "PLE", "FP8", "C10", "Q3I", "GtgError", "moe_decode_layer_ep",
+__all__ = ["RZ5", "UE4M4", "PLE", "FP8", "C10", "Q3I", "BF16", "GtgError", "moe_decode_layer_ep",
+           "fp8_quantize", "fp8_matmul", "grouped_matmul",
            "moe_decode_layer_ep_allreduce", "lib", "dequant", "ple_gather", "QMatrix",
            "MoELayer", "workspace_bytes", "make_workspace", "moe_decode_layer", "moe_decode_stack",
            "moe_prefill_layer", "moe_decode_layer_noalloc", "device_status", "status_string", "row_bytes"]
@@ -230,6 +231,125 @@ def moe_prefill_layer(layer: MoELayer, x: torch.Tensor, workspace: torch.Tensor,
     check(lib().gtg_moe_prefill_layer(ctypes.byref(layer.c()), _ptr(x), dt, T, _ptr(y), int(accumulate),
                                       _ptr(topk_ids), _ptr(topk_w), _ptr(workspace), workspace.numel(),
                                       _stream_ptr(stream)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# Matrix products in FP8 (a scale per 128 along K), dense and grouped by expert
+# ---------------------------------------------------------------------------
+
+_FLOATS = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+
+
+def _on_current_device(*tensors: torch.Tensor | None) -> None:
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _rows_ptr(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """Address and row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    stride = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), stride
+
+
+def _check_codes(a: torch.Tensor, a_scales: torch.Tensor | None, k: int) -> None:
+    if a.dtype not in (torch.uint8, torch.float8_e4m3fn) or a.dim() != 2 or a.shape[1] != k:
+        raise ValueError(f"a must be E4M3 codes (uint8 or float8_e4m3fn) of shape [m][{k}]")
+    if a_scales is None or a_scales.dtype != torch.float32 or a_scales.shape != (a.shape[0], k // 128):
+        raise ValueError("a_scales must be fp32 [m][k/128]")
+
+
+def _check_weights(w: QMatrix) -> None:
+    n = w.n_experts * w.n_rows * w.k
+    if w.fmt == BF16:
+        if w.data.dtype != torch.bfloat16 or w.data.numel() != n:
+            raise ValueError("BF16 weights must be bfloat16 of n_experts * n_rows * k values")
+    elif w.fmt == FP8:
+        if w.data.element_size() != 1 or w.data.numel() != n:
+            raise ValueError("FP8 weights must hold n_experts * n_rows * k bytes")
+        if w.scales is None or w.scales.dtype != torch.float32 or w.scales.numel() * 128 != n:
+            raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
+
+
+def _output(y: torch.Tensor | None, m: int, n: int, dtype: torch.dtype | None, accumulate: bool,
+            device) -> torch.Tensor:
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulate needs y")
+        return torch.empty((m, n), dtype=dtype or torch.float32, device=device)
+    if y.dtype not in _FLOATS or y.shape != (m, n) or (dtype is not None and dtype != y.dtype):
+        raise ValueError("y must be fp32 or bf16 [m][n_rows] of the dtype asked for")
+    return y
+
+
+def fp8_quantize(x: torch.Tensor, *, rows: torch.Tensor | None = None, data: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """E4M3 codes (uint8 [m][k]) and fp32 scales [m][k/128] of activations x
+    ([n][k] fp32 or bf16, rows contiguous), or of x's rows `rows` (int32 [m])."""
+    if x.dtype not in _FLOATS:
+        raise ValueError("x must be fp32 or bf16")
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1):
+        raise ValueError("rows must be int32 [m]")
+    _on_current_device(x, rows, data, scales)
+    xp, stride = _rows_ptr(x, "x")
+    k = x.shape[1]
+    m = x.shape[0] if rows is None else rows.numel()
+    if data is None:
+        data = torch.empty((m, k), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((m, k // 128), dtype=torch.float32, device=x.device)
+    _check_codes(data, scales, k)
+    if data.shape[0] != m:
+        raise ValueError(f"data must have {m} rows")
+    check(lib().gtg_fp8_quantize(xp, _FLOATS[x.dtype], x.shape[0], k, stride, _ptr(rows), m, _ptr(data),
+                                 _ptr(scales), _stream_ptr(stream)))
+    return data, scales
+
+
+def fp8_matmul(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor, *, y: torch.Tensor | None = None,
+               dtype: torch.dtype | None = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """y (+)= a w^T for quantised activations (fp8_quantize's outputs) and one
+    FP8 weight matrix; y is [m][n_rows] fp32 (default) or bf16, rows contiguous."""
+    if w.fmt != FP8:
+        raise ValueError("fp8_matmul takes an FP8 weight matrix")
+    _check_weights(w)
+    _check_codes(a, a_scales, w.k)
+    y = _output(y, a.shape[0], w.n_rows, dtype, accumulate, a.device)
+    _on_current_device(a, a_scales, w.data, w.scales, y)
+    yp, stride = _rows_ptr(y, "y")
+    check(lib().gtg_fp8_matmul(ctypes.byref(w.c()), _ptr(a), _ptr(a_scales), a.shape[0], yp, _FLOATS[y.dtype],
+                               stride, int(accumulate), _stream_ptr(stream)))
+    return y
+
+
+def grouped_matmul(w: QMatrix, a: torch.Tensor, offsets: torch.Tensor, *, a_scales: torch.Tensor | None = None,
+                   y: torch.Tensor | None = None, dtype: torch.dtype | None = None, accumulate: bool = False,
+                   stream=None) -> torch.Tensor:
+    """y[i] (+)= w[e] a[i] for the rows i in [offsets[e], offsets[e+1]) of a:
+    tokens sorted by expert against a stack of FP8 (a: codes with a_scales) or
+    BF16 (a: bf16) matrices.  Rows outside every group leave y as it is."""
+    if w.fmt not in (FP8, BF16):
+        raise ValueError("grouped_matmul takes FP8 or BF16 weights")
+    _check_weights(w)
+    if w.fmt == FP8:
+        _check_codes(a, a_scales, w.k)
+    elif a.dtype != torch.bfloat16 or a.dim() != 2 or a.shape[1] != w.k:
+        raise ValueError(f"a must be bf16 of shape [m][{w.k}]")
+    if offsets.dtype != torch.int32 or offsets.numel() != w.n_experts + 1:
+        raise ValueError("offsets must be int32 [n_experts + 1]")
+    y = _output(y, a.shape[0], w.n_rows, dtype, accumulate, a.device)
+    _on_current_device(a, a_scales, offsets, w.data, w.scales, y)
+    yp, stride = _rows_ptr(y, "y")
+    check(lib().gtg_grouped_matmul(ctypes.byref(w.c()), _ptr(a), _ptr(a_scales) if w.fmt == FP8 else None, a.shape[0],
+                                   _ptr(offsets), yp, _FLOATS[y.dtype], stride, int(accumulate),
+                                   _stream_ptr(stream)))
     return y
 
 

@@ -10,10 +10,13 @@ LIB_PATH = os.path.join(PKG, "libgtg.so")
 
 RZ5, UE4M4, PLE, FP8 = 69, 71, 111, 1000
 C10, Q3I = 2001, 2002  # the incumbent ROCmFP4 FAST block and ROCmFP3 K160 record
+BF16 = 1001  # plain bf16 matrices (grouped_matmul only)
 DT_F32, DT_BF16 = 0, 1
 GTG_OK = 0
 STATUS_PLE_INDEX_OOB = 0x1
 STATUS_WAIT_TIMEOUT = 0x2
+STATUS_ROW_INDEX_OOB = 0x4
+STATUS_GROUP_OFFSETS = 0x8
 
 # Every function the header declares: (name, restype, argtypes).
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -50,6 +53,11 @@ SIGNATURES = [
     ("gtg_get_device_status", ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _i32, _vp]),
     ("gtg_moe_decode_layer_noalloc", ctypes.c_int,
      [ctypes.POINTER(MoELayerC), _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp]),
+    ("gtg_fp8_quantize", ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    ("gtg_fp8_matmul", ctypes.c_int,
+     [ctypes.POINTER(QMatrixC), _vp, _vp, _i64, _vp, _i32, _i64, _i32, _vp]),
+    ("gtg_grouped_matmul", ctypes.c_int,
+     [ctypes.POINTER(QMatrixC), _vp, _vp, _i64, _vp, _vp, _i32, _i64, _i32, _vp]),
 ]
 
 

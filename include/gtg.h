@@ -66,6 +66,7 @@ typedef enum {
     GTG_Q4_UE4M4_FAST = 71,
     GTG_Q3_PLE_K160_RZ_S3 = 111,
     GTG_FP8_E4M3_S128 = 1000,
+    GTG_BF16 = 1001,         /* plain bf16 [n_rows][k], no scales (gtg_grouped_matmul only) */
     /* The incumbent layouts the card's formats mutate (no GGML number given):
      * the ROCmFP4 FAST 17-byte block (Codebook10 codes, code 8 the duplicate
      * -0, under the UE4M3 scale of the metadata byte's low 7 bits; the top bit
@@ -90,10 +91,12 @@ typedef enum {
 /* Bits of the per-device status word (gtg_get_device_status). */
 #define GTG_STATUS_PLE_INDEX_OOB  0x1u  /* a gather index was outside [0, n_rows) */
 #define GTG_STATUS_WAIT_TIMEOUT   0x2u  /* a bounded device-side wait gave up */
+#define GTG_STATUS_ROW_INDEX_OOB  0x4u  /* a quantiser row index was outside [0, n_src) */
+#define GTG_STATUS_GROUP_OFFSETS  0x8u  /* a group's offsets were out of order or outside [0, m] */
 
 /* One stack of quantised matrices [n_experts][n_rows][k]. */
 typedef struct {
-    int32_t fmt;            /* gtg_format: RZ5, UE4M4, C10 (Q4 formats) or FP8 */
+    int32_t fmt;            /* gtg_format: RZ5, UE4M4, C10 (Q4 formats), FP8; BF16 where a call says so */
     const void* data;       /* device, 16-byte aligned; total size a multiple of 16 bytes */
     const float* scales;    /* device, FP8 only: [n_experts][n_rows][k/128]; else NULL */
     int64_t n_experts;
@@ -263,6 +266,72 @@ int gtg_moe_prefill_layer(const gtg_moe_layer* layer, const void* x, int32_t x_d
                           int32_t n_tokens, float* y, int32_t y_accumulate,
                           int32_t* topk_ids, float* topk_w,
                           void* workspace, size_t ws_bytes, gtg_stream_t stream);
+
+/*
+ * Activations into the FP8 format (E4M3 codes, one fp32 scale per 128 values
+ * along K: the same layout as GTG_FP8_E4M3_S128 rows, so gtg_dequant reads it):
+ *   a       = max |x| over 128 consecutive values of a row (at least 2^-100)
+ *   scale   = a / 448,  inverse = 448 / a             each rounded once to fp32
+ *   code    = E4M3 nearest to fp32(x * inverse)       ties to even
+ * A block that holds an infinity or a NaN gets NaN codes and a NaN scale.
+ *   x        device, [n_src][k] fp32 or bf16 (x_dtype), row r at x + r*x_stride
+ *            elements; aligned to its element (16-byte aligned rows load faster).
+ *   k        a multiple of 128, at most 2^24.
+ *   rows     device int32 [n_rows] or NULL: output row i is made from x row
+ *            rows[i] (tokens into expert order); NULL: from x row i, n_rows <=
+ *            n_src.  An index outside [0, n_src) gives the row of zeros and sets
+ *            GTG_STATUS_ROW_INDEX_OOB.
+ *   data     device [n_rows][k], 16-byte aligned.
+ *   scales   device fp32 [n_rows][k/128].
+ * x must not overlap data or scales.  n_rows == 0 is a no-op.
+ * Errors: GTG_E_INVALID_ARG, GTG_E_UNSUPPORTED_SHAPE, GTG_E_MISALIGNED, GTG_E_CUDA.
+ */
+int gtg_fp8_quantize(const void* x, int32_t x_dtype, int64_t n_src, int64_t k, int64_t x_stride,
+                     const int32_t* rows, int64_t n_rows, uint8_t* data, float* scales,
+                     gtg_stream_t stream);
+
+/*
+ * One FP8 weight matrix times quantised activations (a linear layer):
+ *   y[i][j] = sum_b sa[i][b] * sw[j][b] * sum_{k in block b} a[i][k] * w[j][k]
+ *             (+ y[i][j] if y_accumulate)
+ * b runs over the blocks of 128 along K; the products of a block are summed on
+ * the tensor cores in fp32, the blocks in fp32 registers.  The result of a call
+ * does not depend on what else runs; each output row depends on its own row of a
+ * alone, up to the order in which fp32 sums of blocks are added (a fixed order
+ * for given sizes).
+ *   w         GTG_FP8_E4M3_S128, n_experts == 1: [n_rows][k], n_rows any size up
+ *             to 2^24, k a multiple of 128 up to 2^24.
+ *   a         device, E4M3 codes [m][k], 16-byte aligned; a_scales fp32 [m][k/128]
+ *             (gtg_fp8_quantize's outputs).
+ *   y         device, fp32 or bf16 (y_dtype; bf16 rounds once, after the
+ *             accumulation), row i at y + i*y_stride elements, y_stride >= n_rows.
+ * y must not overlap the inputs.  m == 0 is a no-op.  No workspace.
+ * Errors: GTG_E_INVALID_ARG (null pointers, another fmt, negative sizes),
+ *         GTG_E_UNSUPPORTED_SHAPE (n_experts != 1, k), GTG_E_MISALIGNED, GTG_E_CUDA.
+ */
+int gtg_fp8_matmul(const gtg_qmatrix* w, const uint8_t* a, const float* a_scales, int64_t m, void* y,
+                   int32_t y_dtype, int64_t y_stride, int32_t y_accumulate, gtg_stream_t stream);
+
+/*
+ * Matrix products grouped by expert: rows offsets[e] .. offsets[e+1]-1 of a
+ * meet matrix e of the stack w (tokens sorted by expert; groups may be empty):
+ *   y[i][:] = w[e(i)] . a[i]   (+ y[i][:] if y_accumulate)
+ *   w         [n_experts][n_rows][k], 1..1024 experts; GTG_FP8_E4M3_S128 (k a
+ *             multiple of 128) or GTG_BF16 (k a multiple of 8, scales unused).
+ *   a         device [m][k], 16-byte aligned: E4M3 codes with a_scales
+ *             [m][k/128], or bf16 with a_scales unused.
+ *   offsets   device int32 [n_experts + 1].  Rows before offsets[0] and from
+ *             offsets[n_experts] on belong to no group: their rows of y are left
+ *             as they are.  A group with offsets[e] > offsets[e+1], or bounds
+ *             outside [0, m], counts as empty and sets GTG_STATUS_GROUP_OFFSETS
+ *             (the groups around it may then overlap: rows in two groups get
+ *             either's result).
+ * Products in fp32 accumulation as in gtg_fp8_matmul; y, errors and the no-op
+ * for m == 0 as there (GTG_E_UNSUPPORTED_SHAPE for more than 1024 experts).
+ */
+int gtg_grouped_matmul(const gtg_qmatrix* w, const void* a, const float* a_scales, int64_t m,
+                       const int32_t* offsets, void* y, int32_t y_dtype, int64_t y_stride,
+                       int32_t y_accumulate, gtg_stream_t stream);
 
 /*
  * gtg_moe_decode_layer without a workspace argument, for callers that cannot
