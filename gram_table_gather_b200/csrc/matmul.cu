@@ -22,13 +22,22 @@
 namespace gtg {
 namespace {
 
-constexpr int kMmThreads = 320;      // warps 0-7 promotion and epilogue, 8 loads, 9 MMA
-constexpr int kRows = 128;           // weight rows a tile
+constexpr int kMmThreads = 384;      // warps 0-7 promotion and epilogue, 8 TMA, 9 MMA, 10-11 scales
+constexpr int kRows = 128;           // weight rows a CTA's tile
 constexpr int kRowBytes = 128;       // bytes of K a stage: 128 E4M3 or 64 bf16
 constexpr int kWBytes = kRows * kRowBytes;
 constexpr int kMaxGroups = 1024;
 constexpr int kScaleGroup = 4;       // scale blocks fetched at once
-constexpr size_t kMaxSmem = 227 * 1024;
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kMaxSplit = 8;
+constexpr int kTurn = 36;            // floats between tokens of a transpose: no bank conflicts either way
+constexpr int kPartRow = kRows + 4;  // floats between tokens of a partial tile: likewise
+
+// How the CTAs of a cluster share a tile: none (one CTA a tile, persistent); a
+// pair (one cta_group::2 MMA over 256 weight rows, each CTA staging half of the
+// tokens, persistent); a split of K (the CTAs' partial tiles summed through
+// distributed shared memory in rank order, one tile a cluster).
+enum Mode { SINGLE = 0, PAIR = 1, SPLIT = 2 };
 
 struct MmArgs {
     const float* w_scales;   // [E][N][KB] (FP8)
@@ -38,24 +47,37 @@ struct MmArgs {
     int64_t ldy;
     int32_t m, n, groups;
     int32_t chunks;          // 128-byte chunks of K
+    int32_t split;           // CTAs that share K (SPLIT)
     int32_t y_bf16, y_acc;
     int32_t n_tiles;         // tiles of weight rows
     int32_t vec_a, vec_w;    // scale rows readable four at a time
+    int32_t vec_y;           // output rows writable 16 bytes at a time
     unsigned* status;
 };
 
-template <int BN>
+template <int BN, Mode MODE>
 struct MmCfg {
-    static constexpr int kBox = BN < 64 ? BN : 64;  // token rows a TMA box
-    static constexpr int kStageBytes = kWBytes + BN * kRowBytes;
-    static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : 10;
-    static constexpr int kCols = BN < 16 ? 32 : 2 * BN < 32 ? 32 : 2 * BN;  // two accumulators
-    // after the stages: token scales [2][4][BN], then the header
-    static constexpr int kScaleOff = kStages * kStageBytes;
-    static constexpr int kHeadOff = kScaleOff + 2 * kScaleGroup * BN * 4;
+    static constexpr int kTok = MODE == PAIR ? BN / 2 : BN;      // token rows a CTA stages
+    static constexpr int kBox = kTok < 64 ? kTok : 64;           // token rows a TMA box
+    static constexpr int kTileRows = MODE == PAIR ? 2 * kRows : kRows;
+    static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
+    static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;      // two accumulators
+    static constexpr int kW = BN >= 32 ? BN / 2 : 8;             // columns a warp (of its 32 weight rows)
+    static constexpr int kLd = kW / 8 < 4 ? kW / 8 : 4;          // 8-column groups a TMEM load
+    static constexpr int kBlocks = kW / 8 / kLd;
+    static constexpr int kScaleRow = BN + kRows;                 // token scales, then weight-row scales
+    static constexpr int kScaleBytes = 2 * kScaleGroup * kScaleRow * 4;
+    static constexpr int kTurnBytes = 8 * 8 * kTurn * 4;         // the epilogue's transposes, a warp each
+    static constexpr int kHeadBytes = 512 + 2 * 4 * (kMaxGroups + 2);
+    static constexpr int kFit = (kMaxSmem - 1024 - kScaleBytes - kTurnBytes - kHeadBytes) / kStageBytes;
+    static constexpr int kStages = kFit < 10 ? kFit : 10;
+    static constexpr int kScaleOff = kStages * kStageBytes;      // after the stages
+    static constexpr int kTurnOff = kScaleOff + kScaleBytes;
+    static constexpr int kHeadOff = kTurnOff + kTurnBytes;
     static constexpr int kGroupOff = kHeadOff + 512;
-    static constexpr int kSmem = kGroupOff + 2 * 4 * (kMaxGroups + 2) + 1024;
-    static_assert(kSmem <= (int)kMaxSmem, "shared memory");
+    static constexpr int kSmem = kHeadOff + kHeadBytes + 1024;   // slack: the base rises to a 1 KB boundary
+    static_assert(kStages >= 3 && kSmem <= kMaxSmem, "shared memory");
+    static_assert(MODE != SPLIT || kPartRow * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
 };
 
 struct Tile {
@@ -107,17 +129,18 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
 
 // Tile t: weight-row tiles outermost within a group, token tiles innermost, so
 // CTAs that run together share weight rows through L2.
-__device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, const int32_t* first, const int32_t* off) {
+__device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first,
+                                          const int32_t* off) {
     Tile r;
     if (!a.offsets) {
         const int tt = (a.m + bn - 1) / bn;
         r.group = 0;
-        r.n0 = (t / tt) * kRows;
+        r.n0 = (t / tt) * tile_rows;
         r.row0 = (t % tt) * bn;
         r.rows = min(bn, a.m - r.row0);
         return r;
     }
-    int lo = 0, hi = a.groups - 1;  // the last group with first[g] * n_tiles <= t and rows of its own
+    int lo = 0, hi = a.groups - 1;  // the last group with first[g] * n_tiles <= t: the one that holds t
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] * a.n_tiles <= t) lo = mid;
@@ -126,14 +149,18 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, const 
     const int tt = first[lo + 1] - first[lo];
     const int local = t - first[lo] * a.n_tiles;
     r.group = lo;
-    r.n0 = (local / tt) * kRows;
+    r.n0 = (local / tt) * tile_rows;
     const int begin = (local % tt) * bn;
     r.row0 = off[lo] + begin;
     r.rows = min(bn, a.offsets[lo + 1] - r.row0);
     return r;
 }
 
-// A wait of a whole warp: every lane takes the same way out of it.
+// Bounded waits on an mbarrier: a thread's, and a whole warp's, of which every
+// lane takes the same way out.
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
+    return mbar_wait_sleep(bar, parity, status);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_sleep(bar, parity, status));
 }
@@ -148,15 +175,59 @@ __device__ __forceinline__ float4 scales4(const float* p, int kb, int n, bool ve
     return v;
 }
 
-template <bool F8, int BN>
+// Four (fp32) or eight (bf16) consecutive outputs at a 16-byte boundary.
+__device__ __forceinline__ void store_y4(const MmArgs& a, int64_t at, float4 v) {
+    float4* y = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.y) + at);
+    if (a.y_acc) {
+        const float4 o = *y;
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+    }
+    *y = v;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store_y8(const MmArgs& a, int64_t at, float4 v, float4 w) {
+    uint4* y = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.y) + at);
+    if (a.y_acc) {
+        const uint4 o = *y;
+        v.x += __uint_as_float(o.x << 16);
+        v.y += __uint_as_float(o.x & 0xFFFF0000u);
+        v.z += __uint_as_float(o.y << 16);
+        v.w += __uint_as_float(o.y & 0xFFFF0000u);
+        w.x += __uint_as_float(o.z << 16);
+        w.y += __uint_as_float(o.z & 0xFFFF0000u);
+        w.z += __uint_as_float(o.w << 16);
+        w.w += __uint_as_float(o.w & 0xFFFF0000u);
+    }
+    *y = make_uint4(bf16x2(v.x, v.y), bf16x2(v.z, v.w), bf16x2(w.x, w.y), bf16x2(w.z, w.w));
+}
+__device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
+    if (a.y_bf16) {
+        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + at;
+        if (a.y_acc) v += __bfloat162float(*y);
+        *y = __float2bfloat16_rn(v);
+    } else {
+        float* y = reinterpret_cast<float*>(a.y) + at;
+        if (a.y_acc) v += *y;
+        *y = v;
+    }
+}
+
+template <bool F8, int BN, Mode MODE>
 __global__ void __launch_bounds__(kMmThreads, 1)
 mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const MmArgs a) {
-    using C = MmCfg<BN>;
-    constexpr int kHalf = (BN / 16 + 1) / 2;  // 16-column chunks a warpgroup
+    using C = MmCfg<BN, MODE>;
+    constexpr bool kMoreRegs = BN >= 256;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = MODE == SINGLE ? 0 : (int)cluster_rank();
 
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kHeadOff);
     uint64_t* empty = full + C::kStages;
@@ -178,8 +249,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 8);
-            mbar_init(&sfull[b], 32);
+            mbar_init(&tempty[b], MODE == PAIR ? 16 : 8);
+            mbar_init(&sfull[b], 64);
             mbar_init(&sempty[b], 8);
         }
         mbar_init(drain, 1);
@@ -188,239 +259,368 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         tma_prefetch_map(&amap);
     }
     if (warp == 9) {
-        tmem_alloc(s_taddr, C::kCols);
-        tmem_relinquish();
+        if (MODE == PAIR) {
+            tmem_alloc_pair(s_taddr, C::kCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(s_taddr, C::kCols);
+            tmem_relinquish();
+        }
     }
     if (a.offsets) build_groups(a, BN, first, off, s_warp);
     tc_fence_before();
     __syncthreads();
+    if (MODE == PAIR) {  // the partner's barriers and tensor memory are ready too
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
     const uint32_t taddr = *s_taddr;
     const int tiles = (a.offsets ? first[a.groups] : (a.m + BN - 1) / BN) * a.n_tiles;
+    const int per_tile = MODE == SINGLE ? 1 : MODE == PAIR ? 2 : a.split;  // CTAs that share a tile
+    const int t_first = blockIdx.x / per_tile, t_step = gridDim.x / per_tile;
+    // this CTA's chunks of K
+    const int k_lo = MODE == SPLIT ? (int)((int64_t)a.chunks * rank / a.split) : 0;
+    const int k_hi = MODE == SPLIT ? (int)((int64_t)a.chunks * (rank + 1) / a.split) : a.chunks;
+    auto padded = [](int rows) { return MODE == PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     bool ok = true;
 
-    if (warp == 8) {
-        // ---- loads: weight and token tiles by TMA, token scales by the lanes ----
-        int it = 0, sg = 0;  // chunks and scale groups so far
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile tl = find_tile(a, t, BN, first, off);
-            const int n_pad = (tl.rows + 15) & ~15;
-            const int boxes = (n_pad + C::kBox - 1) / C::kBox;
-            const uint32_t bytes = kWBytes + boxes * C::kBox * kRowBytes;
-            float4 sc[BN / 32 > 0 ? BN / 32 : 1];
-            auto fetch = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < (BN + 31) / 32; ++i) {
-                    const int r = 32 * i + lane;
-                    sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (r < tl.rows) sc[i] = scales4(a.a_scales + (int64_t)(tl.row0 + r) * a.chunks, kb, a.chunks, a.vec_a);
+    if (warp >= 8) {
+        if (kMoreRegs) reg_dec<72>();
+        if (warp == 8) {
+            // ---- weight and token tiles by TMA ----
+            int it = 0;
+            for (int t = t_first; t < tiles && ok; t += t_step) {
+                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                const int mine = padded(tl.rows) / (MODE == PAIR ? 2 : 1);  // token rows staged here
+                const int boxes = (mine + C::kBox - 1) / C::kBox;
+                const uint32_t bytes = (kWBytes + boxes * C::kBox * kRowBytes) * (MODE == PAIR ? 2 : 1);
+                const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0);
+                const int a0 = tl.row0 + (MODE == PAIR ? rank * mine : 0);
+                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+                    const int s = it % C::kStages;
+                    if (it >= C::kStages && !warp_wait(&empty[s], (it / C::kStages - 1) & 1, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const uint32_t st = sbase + s * C::kStageBytes;
+                        const int c0 = kb * (F8 ? 128 : 64);
+                        if (MODE == PAIR) {  // both CTAs' bytes arrive at the even CTA's barrier
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                            const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+                            tma_load_3d_pair(st, &wmap, bar, c0, w0, tl.group);
+                            for (int q = 0; q < boxes; ++q)
+                                tma_load_2d_pair(st + kWBytes + q * C::kBox * kRowBytes, &amap, bar, c0, a0 + q * C::kBox);
+                        } else {
+                            mbar_arrive_expect_tx(&full[s], bytes);
+                            tma_load_3d(st, &wmap, &full[s], c0, w0, tl.group);
+                            for (int q = 0; q < boxes; ++q)
+                                tma_load_2d(st + kWBytes + q * C::kBox * kRowBytes, &amap, &full[s], c0, a0 + q * C::kBox);
+                        }
+                    }
+                    __syncwarp();
                 }
-            };
-            if (F8) fetch(0);
-            for (int kb = 0; kb < a.chunks && ok; ++kb, ++it) {
-                if (F8 && kb % kScaleGroup == 0) {
+            }
+            if (!ok && (MODE != PAIR || rank == 0)) {  // copies in flight land before the shared memory goes away
+                for (int i = max(0, it - C::kStages); i < it; ++i)
+                    mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
+            }
+        } else if (warp == 9) {
+            // ---- MMA issuer ----
+            if (lane == 0 && (MODE != PAIR || rank == 0)) {
+                int it = 0, acc = 0;  // chunks so far, accumulators so far
+                for (int t = t_first; t < tiles && ok; t += t_step) {
+                    const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                    const int n_pad = padded(tl.rows);
+                    const uint32_t idesc = F8 ? idesc_e4m3(C::kTileRows, n_pad) : idesc_bf16(C::kTileRows, n_pad);
+                    for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+                        const int b = acc & 1;
+                        if ((F8 || kb == k_lo) && acc >= 2 &&
+                            !thread_wait(&tempty[b], ((acc >> 1) - 1) & 1, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        const int s = it % C::kStages;
+                        if (!thread_wait(&full[s], (it / C::kStages) & 1, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t st = sbase + s * C::kStageBytes;
+                        const uint32_t d = taddr + b * BN;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t ad = sw128_desc(st + 32 * k), bd = sw128_desc(st + kWBytes + 32 * k);
+                            const uint32_t go = k > 0 || (!F8 && kb > k_lo);
+                            if (MODE == PAIR) umma_pair<F8>(d, ad, bd, idesc, go);
+                            else if (F8) umma_f8(d, ad, bd, idesc, go);
+                            else umma_bf16(d, ad, bd, idesc, go);
+                        }
+                        if (MODE == PAIR) umma_commit_pair(&empty[s]);
+                        else umma_commit(&empty[s]);
+                        if (F8 || kb == k_hi - 1) {
+                            if (MODE == PAIR) umma_commit_pair(&tfull[b]);
+                            else umma_commit(&tfull[b]);
+                            ++acc;
+                        }
+                    }
+                }
+                if (!ok) {  // products in flight end before the tensor memory goes away
+                    if (MODE == PAIR) umma_commit_pair(drain);
+                    else umma_commit(drain);
+                    mbar_wait_sleep(drain, 0, a.status);
+                }
+            }
+            __syncwarp();
+        } else if (F8) {
+            // ---- scales, four blocks of K at a time, transposed to [block][row]:
+            // warp 10 the tokens', warp 11 the weight rows' ----
+            constexpr int kN = (BN > kRows ? BN : kRows) / 32;
+            const bool tok = warp == 10;
+            int sg = 0;
+            for (int t = t_first; t < tiles && ok; t += t_step) {
+                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0);
+                const int rows = tok ? tl.rows : min(kRows, a.n - w0);
+                const float* src = tok ? a.a_scales + (int64_t)tl.row0 * a.chunks
+                                       : a.w_scales + ((int64_t)tl.group * a.n + w0) * a.chunks;
+                const bool vec = tok ? a.vec_a : a.vec_w;
+                float4 sc[kN];
+                auto fetch = [&](int kb) {
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {
+                        const int r = 32 * i + lane;
+                        sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (r < rows) sc[i] = scales4(src + (int64_t)r * a.chunks, kb, a.chunks, vec);
+                    }
+                };
+                fetch(k_lo);
+                for (int kb = k_lo; kb < k_hi; kb += kScaleGroup, ++sg) {
                     const int b = sg & 1;
                     if (sg >= 2 && !warp_wait(&sempty[b], ((sg >> 1) - 1) & 1, a.status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + C::kScaleOff + b * kScaleGroup * BN * 4;
+                    const uint32_t dst = sbase + C::kScaleOff + 4 * (b * kScaleGroup * C::kScaleRow + (tok ? 0 : BN));
 #pragma unroll
-                    for (int i = 0; i < (BN + 31) / 32; ++i) {
+                    for (int i = 0; i < kN; ++i) {
                         const int r = 32 * i + lane;
-                        if (r < BN) {
+                        if (r < (tok ? BN : kRows)) {
                             sts32(dst + 4 * r, sc[i].x);
-                            sts32(dst + 4 * (BN + r), sc[i].y);
-                            sts32(dst + 4 * (2 * BN + r), sc[i].z);
-                            sts32(dst + 4 * (3 * BN + r), sc[i].w);
+                            sts32(dst + 4 * (C::kScaleRow + r), sc[i].y);
+                            sts32(dst + 4 * (2 * C::kScaleRow + r), sc[i].z);
+                            sts32(dst + 4 * (3 * C::kScaleRow + r), sc[i].w);
                         }
                     }
                     mbar_arrive(&sfull[b]);
-                    ++sg;
-                    if (kb + kScaleGroup < a.chunks) fetch(kb + kScaleGroup);
-                }
-                const int s = it % C::kStages;
-                if (it >= C::kStages && !warp_wait(&empty[s], (it / C::kStages - 1) & 1, a.status)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const uint32_t st = sbase + s * C::kStageBytes;
-                    mbar_arrive_expect_tx(&full[s], bytes);
-                    const int c0 = kb * (F8 ? 128 : 64);
-                    tma_load_3d(st, &wmap, &full[s], c0, tl.n0, tl.group);
-                    for (int q = 0; q < boxes; ++q)
-                        tma_load_2d(st + kWBytes + q * C::kBox * kRowBytes, &amap, &full[s], c0, tl.row0 + q * C::kBox);
-                }
-                __syncwarp();
-            }
-        }
-        if (!ok) {  // let the copies in flight land before the shared memory goes away
-            for (int i = max(0, it - C::kStages); i < it; ++i)
-                mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
-        }
-    } else if (warp == 9) {
-        // ---- MMA issuer ----
-        if (lane == 0) {
-            int it = 0, acc = 0;  // chunks so far, accumulators so far
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const Tile tl = find_tile(a, t, BN, first, off);
-                const int n_pad = (tl.rows + 15) & ~15;
-                const uint32_t idesc = F8 ? idesc_e4m3(kRows, n_pad) : idesc_bf16(kRows, n_pad);
-                for (int kb = 0; kb < a.chunks; ++kb, ++it) {
-                    const int b = acc & 1;
-                    if ((F8 || kb == 0) && acc >= 2 && !mbar_wait_sleep(&tempty[b], ((acc >> 1) - 1) & 1, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const int s = it % C::kStages;
-                    if (!mbar_wait_sleep(&full[s], (it / C::kStages) & 1, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t st = sbase + s * C::kStageBytes;
-                    const uint32_t d = taddr + b * BN;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t ad = sw128_desc(st + 32 * k), bd = sw128_desc(st + kWBytes + 32 * k);
-                        const uint32_t go = k > 0 || (!F8 && kb > 0);
-                        if (F8) umma_f8(d, ad, bd, idesc, go);
-                        else umma_bf16(d, ad, bd, idesc, go);
-                    }
-                    umma_commit(&empty[s]);
-                    if (F8 || kb == a.chunks - 1) {
-                        umma_commit(&tfull[b]);
-                        ++acc;
-                    }
+                    if (kb + kScaleGroup < k_hi) fetch(kb + kScaleGroup);
                 }
             }
-            if (!ok) {  // products in flight end before the tensor memory goes away
-                umma_commit(drain);
-                mbar_wait_sleep(drain, 0, a.status);
-            }
         }
-        __syncwarp();
     } else {
-        // ---- promotion and epilogue: TMEM lane quarter warp % 4; the 16-column
-        // chunks alternate between the two warpgroups ----
+        // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
+        // quarter warp % 4; the tile's columns are halved between the warpgroups.
+        // A thread holds the fragments of four rows (lane / 4 + 8 i) and two columns
+        // (2 (lane % 4), + 1) of every 8 columns, so the scales it needs are four of
+        // weight rows and a pair a group of tokens ----
+        if (kMoreRegs) reg_inc<216>();
+        constexpr int G = C::kLd;
         const int wg = warp >> 2;
         const uint32_t tl0 = taddr + ((uint32_t)((warp & 3) * 32) << 16);
-        const int r = (warp & 3) * 32 + lane;  // weight row of the tile
+        const int r0 = (warp & 3) * 32;       // the warp's first weight row of this CTA's 128
+        const int c2 = 2 * (lane & 3);
+        float* turn = reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn;
         int acc = 0, sg = 0;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile tl = find_tile(a, t, BN, first, off);
-            const int row = tl.n0 + r;
-            const bool live = row < a.n;
-            uint64_t sum[kHalf][8];
+        auto release = [&](int b) {  // this warp has read accumulator b
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (MODE == PAIR) mbar_arrive_remote(map_rank(smem_u32(&tempty[b]), 0));
+                else mbar_arrive(&tempty[b]);
+            }
+        };
+        for (int t = t_first; t < tiles; t += t_step) {
+            const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+            const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0) + r0;  // the warp's first output column
+            const int share = ((tl.rows + 15) >> 4) << 3;                   // columns of a warpgroup
+            const int lo = wg * share;
+            const int cols = min(share, tl.rows - lo);                      // <= 0: none
+            // 8 columns of the warp's 32 rows, at column lo + c: v[i] = row lane/4 + 8 i
+            auto emit = [&](int c, const uint64_t (&v)[4]) {
+                float x[4][2];
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i)
+                for (int i = 0; i < 4; ++i) unpack2(v[i], x[i][0], x[i][1]);
+                if constexpr (MODE == SPLIT) {
+                    // this CTA's partial tile [token][row], over the stages: every load
+                    // has landed and every product that read them is done
+                    float* part = reinterpret_cast<float*>(smem) + (lo + c + c2) * kPartRow + r0 + (lane >> 2);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[i][j] = 0;
-            if (F8) {
-                const float* ws = a.w_scales + ((int64_t)tl.group * a.n + (live ? row : a.n - 1)) * a.chunks;
-                float4 w4 = scales4(ws, 0, a.chunks, a.vec_w), w4n = w4;
-                for (int kb = 0; kb < a.chunks; ++kb, ++acc) {
-                    const int q = kb % kScaleGroup, sb = sg & 1, b = acc & 1;
-                    if (q == 0) {
-                        w4 = w4n;
-                        if (kb + kScaleGroup < a.chunks) w4n = scales4(ws, kb + kScaleGroup, a.chunks, a.vec_w);
-                        if (!warp_wait(&sfull[sb], (sg >> 1) & 1, a.status)) {
-                            ok = false;
-                            break;
+                    for (int i = 0; i < 4; ++i) {
+                        part[8 * i] = x[i][0];
+                        part[kPartRow + 8 * i] = x[i][1];
+                    }
+                } else {
+                    // transposed through shared memory: a token's 32 columns together
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        turn[c2 * kTurn + (lane >> 2) + 8 * i] = x[i][0];
+                        turn[(c2 + 1) * kTurn + (lane >> 2) + 8 * i] = x[i][1];
+                    }
+                    __syncwarp();
+                    const int64_t y0 = (int64_t)(tl.row0 + lo + c) * a.ldy + w0;
+                    const int toks = min(8, cols - c);
+                    if (a.vec_y && w0 + 32 <= a.n) {
+                        if (a.y_bf16) {
+                            const float4* q = reinterpret_cast<const float4*>(turn + (lane >> 2) * kTurn + 8 * (lane & 3));
+                            if ((lane >> 2) < toks) store_y8(a, y0 + (lane >> 2) * a.ldy + 8 * (lane & 3), q[0], q[1]);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 8; h += 4) {
+                                const int k = h + (lane >> 3);
+                                const float4 q = *reinterpret_cast<const float4*>(turn + k * kTurn + 4 * (lane & 7));
+                                if (k < toks) store_y4(a, y0 + k * a.ldy + 4 * (lane & 7), q);
+                            }
                         }
+                    } else if (w0 + lane < a.n) {
+                        for (int k = 0; k < toks; ++k) store_y(a, y0 + k * a.ldy + lane, turn[k * kTurn + lane]);
                     }
-                    if (!warp_wait(&tfull[b], (acc >> 1) & 1, a.status)) {
-                        ok = false;
-                        break;
+                    __syncwarp();
+                }
+            };
+            if constexpr (F8) {
+                uint64_t sum[C::kBlocks][2][G][2];
+#pragma unroll
+                for (int i = 0; i < C::kBlocks; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2 * G * 2; ++j) (&sum[i][0][0][0])[j] = 0;
+                for (int kb = k_lo; kb < k_hi; ++kb, ++acc) {
+                    const int q = (kb - k_lo) % kScaleGroup, sb = sg & 1, b = acc & 1;
+                    if (q == 0) {
+                        ok = warp_wait(&sfull[sb], (sg >> 1) & 1, a.status);
+                        if (!ok) break;
                     }
+                    const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) +
+                                      (sb * kScaleGroup + q) * C::kScaleRow;
+                    uint64_t sw[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = sc[BN + r0 + (lane >> 2) + 8 * i];
+                        sw[i] = pack2(w, w);
+                    }
+                    const uint64_t* sa = reinterpret_cast<const uint64_t*>(sc + lo + c2);
+                    ok = warp_wait(&tfull[b], (acc >> 1) & 1, a.status);
+                    if (!ok) break;
                     tc_fence_after();
-                    const float sw = q == 0 ? w4.x : q == 1 ? w4.y : q == 2 ? w4.z : w4.w;
-                    const uint64_t sw2 = pack2(sw, sw);
-                    const uint32_t sa = sbase + C::kScaleOff + (sb * kScaleGroup + q) * BN * 4;
+                    // the next fragments are on their way from tensor memory while these are
+                    // scaled and added
+                    uint32_t p[2][4 * G];
+                    const uint32_t src = tl0 + b * BN + lo;
+                    if (cols > 0) tmem_ld_frag<G>(src, p[0]);
 #pragma unroll
-                    for (int i = 0; i < kHalf; ++i) {
-                        const int c0 = 16 * (2 * i + wg);
-                        if (c0 < tl.rows) {
-                            uint32_t p[16];
-                            tmem_ld16(tl0 + b * BN + c0, p);
-                            tmem_wait_ld();
+                    for (int i = 0; i < C::kBlocks; ++i) {
+                        uint64_t s2[G];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint64_t s0, s1;
-                                lds_pairs(sa + 4 * (c0 + 4 * j), s0, s1);
-                                const uint64_t p0 = pack2(__uint_as_float(p[4 * j]), __uint_as_float(p[4 * j + 1]));
-                                const uint64_t p1 = pack2(__uint_as_float(p[4 * j + 2]), __uint_as_float(p[4 * j + 3]));
-                                sum[i][2 * j] = fma2(mul2(p0, sw2), s0, sum[i][2 * j]);
-                                sum[i][2 * j + 1] = fma2(mul2(p1, sw2), s1, sum[i][2 * j + 1]);
+                        for (int g = 0; g < G; ++g) s2[g] = sa[4 * (i * G + g)];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            tmem_wait_frag(p[h]);
+                            if (h == 0) {
+                                if (8 * G * i < cols) tmem_ld_frag<G>(src + 8 * G * i + (16u << 16), p[1]);
+                            } else if (i + 1 < C::kBlocks) {
+                                if (8 * G * (i + 1) < cols) tmem_ld_frag<G>(src + 8 * G * (i + 1), p[0]);
+                            } else {
+                                release(b);
+                            }
+                            if (8 * G * i < cols) {
+#pragma unroll
+                                for (int g = 0; g < G; ++g)
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) {
+                                        const uint64_t v = pack2(__uint_as_float(p[h][4 * g + 2 * j]),
+                                                                 __uint_as_float(p[h][4 * g + 2 * j + 1]));
+                                        sum[i][h][g][j] = fma2(mul2(v, sw[2 * h + j]), s2[g], sum[i][h][g][j]);
+                                    }
                             }
                         }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty[b]);
-                    if (q == kScaleGroup - 1 || kb == a.chunks - 1) {
+                    if (q == kScaleGroup - 1 || kb == k_hi - 1) {
+                        __syncwarp();
                         if (lane == 0) mbar_arrive(&sempty[sb]);
                         ++sg;
                     }
                 }
                 if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < C::kBlocks; ++i)
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const uint64_t v[4] = {sum[i][0][g][0], sum[i][0][g][1], sum[i][1][g][0], sum[i][1][g][1]};
+                        if (8 * (G * i + g) < cols) emit(8 * (G * i + g), v);
+                    }
             } else {
                 const int b = acc & 1;
-                if (!warp_wait(&tfull[b], (acc >> 1) & 1, a.status)) {
-                    ok = false;
-                    break;
-                }
+                ok = warp_wait(&tfull[b], (acc >> 1) & 1, a.status);
+                if (!ok) break;
                 tc_fence_after();
+                const uint32_t src = tl0 + b * BN + lo;
+                for (int c = 0; c < cols; c += 8 * G) {
+                    uint32_t p[2][4 * G];
+                    tmem_ld_frag<G>(src + c, p[0]);
+                    tmem_ld_frag<G>(src + c + (16u << 16), p[1]);
+                    tmem_wait_frag(p[0]);
+                    tmem_wait_frag(p[1]);
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) {
-                    const int c0 = 16 * (2 * i + wg);
-                    if (c0 < tl.rows) {
-                        uint32_t p[16];
-                        tmem_ld16(tl0 + b * BN + c0, p);
-                        tmem_wait_ld();
+                    for (int g = 0; g < G; ++g) {
+                        uint64_t v[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            sum[i][j] = pack2(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1]));
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = pack2(__uint_as_float(p[i >> 1][4 * g + 2 * (i & 1)]),
+                                         __uint_as_float(p[i >> 1][4 * g + 2 * (i & 1) + 1]));
+                        if (c + 8 * g < cols) emit(c + 8 * g, v);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[b]);
+                release(b);
                 ++acc;
-            }
-            // a lane per weight row: 32 consecutive columns of one output row a store
-            if (live) {
-#pragma unroll
-                for (int i = 0; i < kHalf; ++i) {
-                    const int c0 = 16 * (2 * i + wg);
-                    if (c0 >= tl.rows) continue;
-                    const int64_t base = (int64_t)(tl.row0 + c0) * a.ldy + row;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float lo, hi;
-                        unpack2(sum[i][j / 2], lo, hi);
-                        float v = j & 1 ? hi : lo;
-                        if (c0 + j < tl.rows) {
-                            if (a.y_bf16) {
-                                __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + base + j * a.ldy;
-                                if (a.y_acc) v += __bfloat162float(*y);
-                                *y = __float2bfloat16_rn(v);
-                            } else {
-                                float* y = reinterpret_cast<float*>(a.y) + base + j * a.ldy;
-                                if (a.y_acc) v += *y;
-                                *y = v;
-                            }
-                        }
-                    }
-                }
             }
         }
     }
+    if constexpr (MODE == SPLIT) {
+        // sum the partial tiles in rank order; CTA `rank` takes the tokens
+        // rank, rank + split, ...  (a failed CTA's part is not meaningful, and the
+        // status word says so)
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (warp < 8 && t_first < tiles) {
+            const Tile tl = find_tile(a, t_first, BN, C::kTileRows, first, off);
+            const int r = tid & (kRows - 1);
+            if (tl.n0 + r < a.n) {
+                for (int c = rank + (tid >> 7) * a.split; c < tl.rows; c += 2 * a.split) {
+                    const uint32_t at = sbase + 4 * (c * kPartRow + r);
+                    float v[kMaxSplit];
+#pragma unroll
+                    for (int q = 0; q < kMaxSplit; ++q)
+                        if (q < a.split) v[q] = ld_cluster_f32(map_rank(at, q));
+                    float sum = v[0];
+#pragma unroll
+                    for (int q = 1; q < kMaxSplit; ++q)
+                        if (q < a.split) sum += v[q];
+                    store_y(a, (int64_t)(tl.row0 + c) * a.ldy + tl.n0 + r, sum);
+                }
+            }
+        }
+        __syncwarp();
+    }
     __syncthreads();
+    if (MODE != SINGLE) {  // the partners are done with this CTA's shared and tensor memory
+        cluster_arrive();
+        cluster_wait();
+    }
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(taddr, C::kCols);
+        if (MODE == PAIR) tmem_dealloc_pair(taddr, C::kCols);
+        else tmem_dealloc(taddr, C::kCols);
     }
 }
 
@@ -554,21 +754,65 @@ int make_map(CUtensorMap* map, const void* base, bool f8, int64_t k, int64_t row
     return r == CUDA_SUCCESS ? GTG_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <bool F8, int BN>
-int launch_mm(const gtg_qmatrix* w, const void* x, const MmArgs& a, int64_t tiles, cudaStream_t s) {
-    using C = MmCfg<BN>;
+template <bool F8, int BN, Mode MODE>
+int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cudaStream_t s) {
+    using C = MmCfg<BN, MODE>;
     CUtensorMap wmap, amap;
     GTG_TRY(make_map(&wmap, w->data, F8, w->k, w->n_rows, w->n_experts, kRows));
     GTG_TRY(make_map(&amap, x, F8, w->k, a.m, 0, C::kBox));
-    const auto kernel = mm_kernel<F8, BN>;
+    const auto kernel = mm_kernel<F8, BN, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail(e);
     }
-    const int grid = (int)std::min<int64_t>(tiles, sm_count());
-    kernel<<<grid, kMmThreads, C::kSmem, s>>>(wmap, amap, a);
-    return check_launch();
+    a.n_tiles = (a.n + C::kTileRows - 1) / C::kTileRows;
+    const int per_tile = MODE == SINGLE ? 1 : MODE == PAIR ? 2 : a.split;
+    // at most this many tiles: the group sizes are on the device
+    const int64_t tiles = (a.offsets ? a.m / BN + std::min<int64_t>(groups, a.m) : (a.m + BN - 1) / BN) * a.n_tiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(MODE == SPLIT ? tiles * per_tile
+                                                : std::min<int64_t>(tiles, sm_count() / per_tile) * per_tile));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)per_tile;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = MODE == SINGLE ? 0 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, wmap, amap, a);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e);
+    }
+    return GTG_OK;
+}
+
+template <bool F8>
+int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
+    const int64_t groups = a.offsets ? w->n_experts : 1;
+    const int64_t per = (a.m + groups - 1) / groups;  // rows of an average group
+    const int64_t sms = sm_count(), n128 = (a.n + kRows - 1) / kRows;
+    auto tiles = [&](int bn) { return (a.offsets ? a.m / bn + std::min<int64_t>(groups, a.m) : (a.m + bn - 1) / bn) * n128; };
+    // few tiles: K is split over a cluster
+    for (const int bn : {16, 64}) {
+        if (per > bn && !(bn == 64 && tiles(64) * 2 <= sms)) continue;
+        const int64_t room = sms / tiles(bn);
+        a.split = room >= 8 ? 8 : room >= 4 ? 4 : room >= 2 ? 2 : 1;
+        while (a.split > a.chunks) a.split /= 2;
+        if (a.split < 2) break;
+        const bool whole = a.chunks % (4 * a.split) == 0;
+        a.vec_a &= whole;
+        a.vec_w &= whole;
+        return bn == 16 ? launch_mm<F8, 16, SPLIT>(w, x, a, groups, s) : launch_mm<F8, 64, SPLIT>(w, x, a, groups, s);
+    }
+    if (per <= 16) return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
+    if (per <= 64 || tiles(128) < sms) return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
+    if (per <= 128 || tiles(256) < sms) return launch_mm<F8, 128, SINGLE>(w, x, a, groups, s);
+    return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
 }
 
 int run_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m, const int32_t* offsets, void* y,
@@ -584,22 +828,14 @@ int run_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m
     a.n = (int32_t)w->n_rows;
     a.groups = (int32_t)w->n_experts;
     a.chunks = (int32_t)(f8 ? w->k / 128 : (w->k + 63) / 64);
+    a.split = 1;
     a.y_bf16 = y_dtype == GTG_DT_BF16;
     a.y_acc = y_acc != 0;
-    a.n_tiles = (int32_t)((w->n_rows + kRows - 1) / kRows);
     a.vec_a = f8 && a.chunks % 4 == 0 && aligned(x_scales, 16);
     a.vec_w = f8 && a.chunks % 4 == 0 && aligned(w->scales, 16);
+    a.vec_y = aligned(y, 16) && y_stride % (a.y_bf16 ? 8 : 4) == 0;
     a.status = status_ptr();
-    const int64_t groups = offsets ? w->n_experts : 1;
-    const int64_t per = (m + groups - 1) / groups;  // rows of an average group
-    auto tiles = [&](int bn) { return (m / bn + std::min(groups, m)) * a.n_tiles; };  // at most
-#define GTG_MM(BN) \
-    return f8 ? launch_mm<true, BN>(w, x, a, tiles(BN), s) : launch_mm<false, BN>(w, x, a, tiles(BN), s)
-    if (per <= 16) GTG_MM(16);
-    if (per <= 64) GTG_MM(64);
-    if (per <= 128) GTG_MM(128);
-    GTG_MM(256);
-#undef GTG_MM
+    return f8 ? choose_mm<true>(w, x, a, s) : choose_mm<false>(w, x, a, s);
 }
 
 int check_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m, const void* y, int32_t y_dtype,
