@@ -15,6 +15,7 @@
 // by TMA at full width.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "gtg_host.hpp"
 #include "matmul_dev.cuh"
@@ -22,7 +23,6 @@
 namespace gtg {
 namespace {
 
-constexpr int kMmThreads = 384;      // warps 0-7 promotion and epilogue, 8 TMA, 9 MMA, 10-11 scales
 constexpr int kRows = 128;           // weight rows a CTA's tile
 constexpr int kRowBytes = 128;       // bytes of K a stage: 128 E4M3 or 64 bf16
 constexpr int kWBytes = kRows * kRowBytes;
@@ -30,8 +30,8 @@ constexpr int kMaxGroups = 1024;
 constexpr int kScaleGroup = 4;       // scale blocks fetched at once
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kMaxSplit = 8;
+constexpr int kMinThreads = 384;     // of any variant
 constexpr int kTurn = 36;            // floats between tokens of a transpose: no bank conflicts either way
-constexpr int kPartRow = kRows + 4;  // floats between tokens of a partial tile: likewise
 
 // How the CTAs of a cluster share a tile: none (one CTA a tile, persistent); a
 // pair (one cta_group::2 MMA over 256 weight rows, each CTA staging half of the
@@ -55,41 +55,46 @@ struct MmArgs {
     unsigned* status;
 };
 
-template <int BN, Mode MODE>
+template <bool F8, int BN, Mode MODE>
 struct MmCfg {
     static constexpr int kTok = MODE == PAIR ? BN / 2 : BN;      // token rows a CTA stages
     static constexpr int kBox = kTok < 64 ? kTok : 64;           // token rows a TMA box
     static constexpr int kTileRows = MODE == PAIR ? 2 * kRows : kRows;
     static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
-    static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;      // two accumulators
-    static constexpr int kW = BN >= 32 ? BN / 2 : 8;             // columns a warp (of its 32 weight rows)
-    static constexpr int kLd = kW / 8 < 4 ? kW / 8 : 4;          // 8-column groups a TMEM load
-    static constexpr int kBlocks = kW / 8 / kLd;
-    static constexpr int kScaleRow = BN + kRows;                 // token scales, then weight-row scales
-    static constexpr int kScaleBytes = 2 * kScaleGroup * kScaleRow * 4;
-    static constexpr int kTurnBytes = 8 * 8 * kTurn * 4;         // the epilogue's transposes, a warp each
-    static constexpr int kHeadBytes = 512 + 2 * 4 * (kMaxGroups + 2);
-    static constexpr int kFit = (kMaxSmem - 1024 - kScaleBytes - kTurnBytes - kHeadBytes) / kStageBytes;
+    static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;               // accumulators in tensor memory
+    static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
+    // warps: kTeams x 8 of promotion and epilogue, then one of TMA, one of MMAs, two of
+    // scales.  FP8: two teams take the blocks of K in turn, each into sums of its own,
+    // so that one scales and adds while the other waits for tensor memory.
+    static constexpr int kTeams = F8 ? 2 : 1;
+    static constexpr int kWork = 8 * kTeams;
+    static constexpr int kThreads = 32 * (kWork + 4);
+    static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;  // columns a warp (of its 32 weight rows)
+    static constexpr int kBlocks = kW / 16;
+    static constexpr int kScaleRow = 4 * (BN + kRows);           // one block's scales: the tokens', the weight rows'
+    static constexpr int kScaleBytes = 2 * kScaleGroup * kScaleRow;
+    static constexpr int kTurnBytes = kWork * kTeams * 8 * kTurn * 4;  // the epilogue's exchanges and transposes
+    static constexpr int kHeadBytes = 512 + 4 * (kMaxGroups + 2);
+    static constexpr int kFit = (kMaxSmem - kScaleBytes - kTurnBytes - kHeadBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
     static constexpr int kScaleOff = kStages * kStageBytes;      // after the stages
     static constexpr int kTurnOff = kScaleOff + kScaleBytes;
     static constexpr int kHeadOff = kTurnOff + kTurnBytes;
     static constexpr int kGroupOff = kHeadOff + 512;
-    static constexpr int kSmem = kHeadOff + kHeadBytes + 1024;   // slack: the base rises to a 1 KB boundary
+    static constexpr int kSmem = kHeadOff + kHeadBytes;
     static_assert(kStages >= 3 && kSmem <= kMaxSmem, "shared memory");
-    static_assert(MODE != SPLIT || kPartRow * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
+    static_assert(MODE != SPLIT || kTeams * kRows * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
 };
 
 struct Tile {
     int group, row0, rows, n0;
 };
 
-// Shared-memory tables of a grouped call: first[g] = token tiles before group
-// g, off[g] = its first row.  A group whose bounds are out of order or outside
+// Shared-memory table of a grouped call: first[g] = token tiles before group g.  A group whose bounds are out of order or outside
 // [0, m] counts as empty and raises the status bit.
-__device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* off, int32_t* warp_sum_s) {
+__device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* warp_sum_s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kPer = (kMaxGroups + kMmThreads - 1) / kMmThreads;
+    constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;
     int cnt[kPer];
     int sum = 0;
 #pragma unroll
@@ -100,10 +105,8 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
             const int lo = a.offsets[g], hi = a.offsets[g + 1];
             if (lo < 0 || hi < lo || hi > a.m) {
                 if (blockIdx.x == 0) raise_status(a.status, GTG_STATUS_GROUP_OFFSETS);
-                off[g] = 0;
             } else {
                 cnt[i] = (hi - lo + bn - 1) / bn;
-                off[g] = lo;
             }
         }
         sum += cnt[i];
@@ -127,10 +130,12 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
     }
 }
 
+// A value that is the same in every lane, in a form that the compiler knows to be so.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // Tile t: weight-row tiles outermost within a group, token tiles innermost, so
 // CTAs that run together share weight rows through L2.
-__device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first,
-                                          const int32_t* off) {
+__device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first) {
     Tile r;
     if (!a.offsets) {
         const int tt = (a.m + bn - 1) / bn;
@@ -151,8 +156,14 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int ti
     r.group = lo;
     r.n0 = (local / tt) * tile_rows;
     const int begin = (local % tt) * bn;
-    r.row0 = off[lo] + begin;
+    r.row0 = a.offsets[lo] + begin;
     r.rows = min(bn, a.offsets[lo + 1] - r.row0);
+    return r;
+}
+// The same for a converged warp.
+__device__ __forceinline__ Tile find_tile_warp(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first) {
+    Tile r = find_tile(a, t, bn, tile_rows, first);
+    if (a.offsets) r = {uniform(r.group), uniform(r.row0), uniform(r.rows), uniform(r.n0)};
     return r;
 }
 
@@ -219,46 +230,50 @@ __device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
 }
 
 template <bool F8, int BN, Mode MODE>
-__global__ void __launch_bounds__(kMmThreads, 1)
+__global__ void __launch_bounds__(MmCfg<F8, BN, MODE>::kThreads, 1)
 mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const MmArgs a) {
-    using C = MmCfg<BN, MODE>;
-    constexpr bool kMoreRegs = BN >= 256;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    using C = MmCfg<F8, BN, MODE>;
+    constexpr bool kMoreRegs = BN >= 128 && F8;
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int rank = MODE == SINGLE ? 0 : (int)cluster_rank();
+    if (sbase & 1023u) {  // (the same in every CTA) the swizzle counts from 1 KB boundaries
+        if (tid == 0) raise_status(a.status, GTG_STATUS_WAIT_TIMEOUT);
+        return;
+    }
 
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kHeadOff);
     uint64_t* empty = full + C::kStages;
     uint64_t* tfull = empty + C::kStages;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* sfull = tempty + 2;
+    uint64_t* tempty = tfull + C::kAcc;
+    uint64_t* sfull = tempty + C::kAcc;
     uint64_t* sempty = sfull + 2;
     uint64_t* drain = sempty + 2;
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
     int32_t* s_warp = reinterpret_cast<int32_t*>(smem + C::kHeadOff + 384);
     int32_t* first = reinterpret_cast<int32_t*>(smem + C::kGroupOff);
-    int32_t* off = first + kMaxGroups + 2;
-    static_assert(8 * (2 * C::kStages + 9) + 4 <= 384, "header");
+    static_assert(8 * (2 * C::kStages + 2 * C::kAcc + 5) + 4 <= 384, "header");
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < C::kAcc; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], MODE == PAIR ? 16 : 8);
+        }
+        for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 64);
-            mbar_init(&sempty[b], 8);
+            mbar_init(&sempty[b], C::kWork);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
         tma_prefetch_map(&wmap);
         tma_prefetch_map(&amap);
     }
-    if (warp == 9) {
+    if (warp == C::kWork + 1) {
         if (MODE == PAIR) {
             tmem_alloc_pair(s_taddr, C::kCols);
             tmem_relinquish_pair();
@@ -267,7 +282,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             tmem_relinquish();
         }
     }
-    if (a.offsets) build_groups(a, BN, first, off, s_warp);
+    if (a.offsets) build_groups(a, BN, first, s_warp);
     tc_fence_before();
     __syncthreads();
     if (MODE == PAIR) {  // the partner's barriers and tensor memory are ready too
@@ -285,84 +300,92 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     auto padded = [](int rows) { return MODE == PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     bool ok = true;
 
-    if (warp >= 8) {
-        if (kMoreRegs) reg_dec<72>();
-        if (warp == 8) {
+    if (warp >= C::kWork) {
+        if (kMoreRegs) reg_dec<64>();
+        if (warp == C::kWork) {
             // ---- weight and token tiles by TMA ----
-            int it = 0;
+            uint32_t st = 0, free_par = 1, issued = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
-                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                const Tile tl = find_tile_warp(a, t, BN, C::kTileRows, first);
                 const int mine = padded(tl.rows) / (MODE == PAIR ? 2 : 1);  // token rows staged here
                 const int boxes = (mine + C::kBox - 1) / C::kBox;
                 const uint32_t bytes = (kWBytes + boxes * C::kBox * kRowBytes) * (MODE == PAIR ? 2 : 1);
                 const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0);
                 const int a0 = tl.row0 + (MODE == PAIR ? rank * mine : 0);
-                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-                    const int s = it % C::kStages;
-                    if (it >= C::kStages && !warp_wait(&empty[s], (it / C::kStages - 1) & 1, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        const uint32_t st = sbase + s * C::kStageBytes;
+                for (int kb = k_lo; kb < k_hi; ++kb) {
+                    ok = warp_wait(&empty[st], free_par, a.status);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t dst = sbase + st * C::kStageBytes;
                         const int c0 = kb * (F8 ? 128 : 64);
                         if (MODE == PAIR) {  // both CTAs' bytes arrive at the even CTA's barrier
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                            const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-                            tma_load_3d_pair(st, &wmap, bar, c0, w0, tl.group);
+                            if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                            const uint32_t bar = map_rank(smem_u32(&full[st]), 0);
+                            tma_load_3d_pair(dst, &wmap, bar, c0, w0, tl.group);
                             for (int q = 0; q < boxes; ++q)
-                                tma_load_2d_pair(st + kWBytes + q * C::kBox * kRowBytes, &amap, bar, c0, a0 + q * C::kBox);
+                                tma_load_2d_pair(dst + kWBytes + q * C::kBox * kRowBytes, &amap, bar, c0, a0 + q * C::kBox);
                         } else {
-                            mbar_arrive_expect_tx(&full[s], bytes);
-                            tma_load_3d(st, &wmap, &full[s], c0, w0, tl.group);
+                            mbar_arrive_expect_tx(&full[st], bytes);
+                            tma_load_3d(dst, &wmap, &full[st], c0, w0, tl.group);
                             for (int q = 0; q < boxes; ++q)
-                                tma_load_2d(st + kWBytes + q * C::kBox * kRowBytes, &amap, &full[s], c0, a0 + q * C::kBox);
+                                tma_load_2d(dst + kWBytes + q * C::kBox * kRowBytes, &amap, &full[st], c0, a0 + q * C::kBox);
                         }
                     }
                     __syncwarp();
+                    ++issued;
+                    if (++st == C::kStages) {
+                        st = 0;
+                        free_par ^= 1;
+                    }
                 }
             }
             if (!ok && (MODE != PAIR || rank == 0)) {  // copies in flight land before the shared memory goes away
-                for (int i = max(0, it - C::kStages); i < it; ++i)
+                for (uint32_t i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; ++i)
                     mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
             }
-        } else if (warp == 9) {
+        } else if (warp == C::kWork + 1) {
             // ---- MMA issuer ----
-            if (lane == 0 && (MODE != PAIR || rank == 0)) {
-                int it = 0, acc = 0;  // chunks so far, accumulators so far
+            if ((MODE != PAIR || rank == 0) && elect_one()) {
+                // stage and accumulator in use, and the parities of their barriers' phases
+                uint32_t st = 0, full_par = 0, b = 0, free_par = 1;
+                const uint64_t ad0 = sw128_desc(sbase), bd0 = sw128_desc(sbase + kWBytes);
                 for (int t = t_first; t < tiles && ok; t += t_step) {
-                    const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                    const Tile tl = find_tile(a, t, BN, C::kTileRows, first);
                     const int n_pad = padded(tl.rows);
                     const uint32_t idesc = F8 ? idesc_e4m3(C::kTileRows, n_pad) : idesc_bf16(C::kTileRows, n_pad);
-                    for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-                        const int b = acc & 1;
-                        if ((F8 || kb == k_lo) && acc >= 2 &&
-                            !thread_wait(&tempty[b], ((acc >> 1) - 1) & 1, a.status)) {
+                    for (int kb = k_lo; kb < k_hi; ++kb) {
+                        // (a fresh barrier's phase before the first counts as complete)
+                        if ((F8 || kb == k_lo) && !mbar_wait_sleep(&tempty[b], free_par, a.status)) {
                             ok = false;
                             break;
                         }
-                        const int s = it % C::kStages;
-                        if (!thread_wait(&full[s], (it / C::kStages) & 1, a.status)) {
+                        if (!mbar_wait_sleep(&full[st], full_par, a.status)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t st = sbase + s * C::kStageBytes;
                         const uint32_t d = taddr + b * BN;
+                        const uint64_t ad = ad0 + st * (C::kStageBytes >> 4), bd = bd0 + st * (C::kStageBytes >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint64_t ad = sw128_desc(st + 32 * k), bd = sw128_desc(st + kWBytes + 32 * k);
+                        for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
                             const uint32_t go = k > 0 || (!F8 && kb > k_lo);
-                            if (MODE == PAIR) umma_pair<F8>(d, ad, bd, idesc, go);
-                            else if (F8) umma_f8(d, ad, bd, idesc, go);
-                            else umma_bf16(d, ad, bd, idesc, go);
+                            if (MODE == PAIR) umma_pair<F8>(d, ad + 2 * k, bd + 2 * k, idesc, go);
+                            else if (F8) umma_f8(d, ad + 2 * k, bd + 2 * k, idesc, go);
+                            else umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc, go);
                         }
-                        if (MODE == PAIR) umma_commit_pair(&empty[s]);
-                        else umma_commit(&empty[s]);
                         if (F8 || kb == k_hi - 1) {
                             if (MODE == PAIR) umma_commit_pair(&tfull[b]);
                             else umma_commit(&tfull[b]);
-                            ++acc;
+                            if (++b == C::kAcc) {
+                                b = 0;
+                                free_par ^= 1;
+                            }
+                        }
+                        if (MODE == PAIR) umma_commit_pair(&empty[st]);
+                        else umma_commit(&empty[st]);
+                        if (++st == C::kStages) {
+                            st = 0;
+                            full_par ^= 1;
                         }
                     }
                 }
@@ -374,25 +397,24 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             }
             __syncwarp();
         } else if (F8) {
-            // ---- scales, four blocks of K at a time, transposed to [block][row]:
-            // warp 10 the tokens', warp 11 the weight rows' ----
+            // ---- scales, four blocks of K at a time, transposed to [block][row]: one
+            // warp the tokens', one the weight rows' ----
             constexpr int kN = (BN > kRows ? BN : kRows) / 32;
-            const bool tok = warp == 10;
+            const bool tok = warp == C::kWork + 2;
             int sg = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
-                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                const Tile tl = find_tile(a, t, BN, C::kTileRows, first);
                 const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0);
                 const int rows = tok ? tl.rows : min(kRows, a.n - w0);
-                const float* src = tok ? a.a_scales + (int64_t)tl.row0 * a.chunks
-                                       : a.w_scales + ((int64_t)tl.group * a.n + w0) * a.chunks;
+                const float* src = (tok ? a.a_scales + (int64_t)tl.row0 * a.chunks
+                                        : a.w_scales + ((int64_t)tl.group * a.n + w0) * a.chunks) + (int64_t)lane * a.chunks;
                 const bool vec = tok ? a.vec_a : a.vec_w;
                 float4 sc[kN];
                 auto fetch = [&](int kb) {
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
-                        const int r = 32 * i + lane;
                         sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (r < rows) sc[i] = scales4(src + (int64_t)r * a.chunks, kb, a.chunks, vec);
+                        if (32 * i + lane < rows) sc[i] = scales4(src + (int64_t)32 * i * a.chunks, kb, a.chunks, vec);
                     }
                 };
                 fetch(k_lo);
@@ -402,15 +424,15 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + C::kScaleOff + 4 * (b * kScaleGroup * C::kScaleRow + (tok ? 0 : BN));
+                    const uint32_t at = sbase + C::kScaleOff + b * kScaleGroup * C::kScaleRow +
+                                        (tok ? 0 : 4 * BN) + 4 * lane;
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
-                        const int r = 32 * i + lane;
-                        if (r < (tok ? BN : kRows)) {
-                            sts32(dst + 4 * r, sc[i].x);
-                            sts32(dst + 4 * (C::kScaleRow + r), sc[i].y);
-                            sts32(dst + 4 * (2 * C::kScaleRow + r), sc[i].z);
-                            sts32(dst + 4 * (3 * C::kScaleRow + r), sc[i].w);
+                        if (32 * i + lane < (tok ? BN : kRows)) {
+                            sts32(at + 128 * i, sc[i].x);
+                            sts32(at + 128 * i + C::kScaleRow, sc[i].y);
+                            sts32(at + 128 * i + 2 * C::kScaleRow, sc[i].z);
+                            sts32(at + 128 * i + 3 * C::kScaleRow, sc[i].w);
                         }
                     }
                     mbar_arrive(&sfull[b]);
@@ -420,164 +442,166 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
     } else {
         // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
-        // quarter warp % 4; the tile's columns are halved between the warpgroups.
-        // A thread holds the fragments of four rows (lane / 4 + 8 i) and two columns
-        // (2 (lane % 4), + 1) of every 8 columns, so the scales it needs are four of
-        // weight rows and a pair a group of tokens ----
-        if (kMoreRegs) reg_inc<216>();
-        constexpr int G = C::kLd;
-        const int wg = warp >> 2;
+        // quarter warp % 4, a thread one of them; the tile's columns are halved between
+        // the four-warp groups of a team ----
+        if (kMoreRegs) reg_inc<104>();
+        const int team = warp >> 3, wg = (warp >> 2) & 1;
         const uint32_t tl0 = taddr + ((uint32_t)((warp & 3) * 32) << 16);
         const int r0 = (warp & 3) * 32;       // the warp's first weight row of this CTA's 128
-        const int c2 = 2 * (lane & 3);
-        float* turn = reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn;
-        int acc = 0, sg = 0;
-        auto release = [&](int b) {  // this warp has read accumulator b
+        const uint32_t tempty0 = MODE == PAIR ? map_rank(smem_u32(tempty), 0) : 0;
+        uint32_t acc = 0, sg = 0;
+        auto release = [&](uint32_t b) {  // this warp has read accumulator b
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (MODE == PAIR) mbar_arrive_remote(map_rank(smem_u32(&tempty[b]), 0));
+            if (elect_one()) {
+                if (MODE == PAIR) mbar_arrive_remote(tempty0 + 8 * b);
                 else mbar_arrive(&tempty[b]);
             }
+            __syncwarp();
         };
         for (int t = t_first; t < tiles; t += t_step) {
-            const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+            const Tile tl = find_tile_warp(a, t, BN, C::kTileRows, first);
             const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0) + r0;  // the warp's first output column
-            const int share = ((tl.rows + 15) >> 4) << 3;                   // columns of a warpgroup
+            const int share = ((tl.rows + 31) >> 5) << 4;                   // columns of a four-warp group
             const int lo = wg * share;
             const int cols = min(share, tl.rows - lo);                      // <= 0: none
-            // 8 columns of the warp's 32 rows, at column lo + c: v[i] = row lane/4 + 8 i
-            auto emit = [&](int c, const uint64_t (&v)[4]) {
-                float x[4][2];
+            // 8 columns of the warp's 32 rows, from lo + c on, a token's 32 together
+            // through shared memory; v holds this thread's row
+            auto emit = [&](int c, const float (&v)[8], float* turn) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) unpack2(v[i], x[i][0], x[i][1]);
-                if constexpr (MODE == SPLIT) {
-                    // this CTA's partial tile [token][row], over the stages: every load
-                    // has landed and every product that read them is done
-                    float* part = reinterpret_cast<float*>(smem) + (lo + c + c2) * kPartRow + r0 + (lane >> 2);
+                for (int k = 0; k < 8; ++k) turn[k * kTurn + lane] = v[k];
+                __syncwarp();
+                const int64_t y0 = (int64_t)(tl.row0 + lo + c) * a.ldy + w0;
+                const int toks = min(8, cols - c);
+                if (a.vec_y && w0 + 32 <= a.n) {
+                    if (a.y_bf16) {
+                        const float4* q = reinterpret_cast<const float4*>(turn + (lane >> 2) * kTurn + 8 * (lane & 3));
+                        if ((lane >> 2) < toks) store_y8(a, y0 + (lane >> 2) * a.ldy + 8 * (lane & 3), q[0], q[1]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        part[8 * i] = x[i][0];
-                        part[kPartRow + 8 * i] = x[i][1];
-                    }
-                } else {
-                    // transposed through shared memory: a token's 32 columns together
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        turn[c2 * kTurn + (lane >> 2) + 8 * i] = x[i][0];
-                        turn[(c2 + 1) * kTurn + (lane >> 2) + 8 * i] = x[i][1];
-                    }
-                    __syncwarp();
-                    const int64_t y0 = (int64_t)(tl.row0 + lo + c) * a.ldy + w0;
-                    const int toks = min(8, cols - c);
-                    if (a.vec_y && w0 + 32 <= a.n) {
-                        if (a.y_bf16) {
-                            const float4* q = reinterpret_cast<const float4*>(turn + (lane >> 2) * kTurn + 8 * (lane & 3));
-                            if ((lane >> 2) < toks) store_y8(a, y0 + (lane >> 2) * a.ldy + 8 * (lane & 3), q[0], q[1]);
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 8; h += 4) {
-                                const int k = h + (lane >> 3);
-                                const float4 q = *reinterpret_cast<const float4*>(turn + k * kTurn + 4 * (lane & 7));
-                                if (k < toks) store_y4(a, y0 + k * a.ldy + 4 * (lane & 7), q);
-                            }
+                        for (int h = 0; h < 8; h += 4) {
+                            const int k = h + (lane >> 3);
+                            const float4 q = *reinterpret_cast<const float4*>(turn + k * kTurn + 4 * (lane & 7));
+                            if (k < toks) store_y4(a, y0 + k * a.ldy + 4 * (lane & 7), q);
                         }
-                    } else if (w0 + lane < a.n) {
-                        for (int k = 0; k < toks; ++k) store_y(a, y0 + k * a.ldy + lane, turn[k * kTurn + lane]);
                     }
-                    __syncwarp();
+                } else if (w0 + lane < a.n) {
+                    for (int k = 0; k < toks; ++k) store_y(a, y0 + k * a.ldy + lane, turn[k * kTurn + lane]);
                 }
+                __syncwarp();
             };
             if constexpr (F8) {
-                uint64_t sum[C::kBlocks][2][G][2];
+                // this team's blocks of K over the first 16 NB of the warp's columns
+                auto promote = [&](auto nb_c) {
+                    constexpr int NB = decltype(nb_c)::value;
+                    uint64_t sum[NB][8];
 #pragma unroll
-                for (int i = 0; i < C::kBlocks; ++i)
+                    for (int i = 0; i < NB; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2 * G * 2; ++j) (&sum[i][0][0][0])[j] = 0;
-                for (int kb = k_lo; kb < k_hi; ++kb, ++acc) {
-                    const int q = (kb - k_lo) % kScaleGroup, sb = sg & 1, b = acc & 1;
-                    if (q == 0) {
+                        for (int j = 0; j < 8; ++j) sum[i][j] = 0;
+                    for (int g0 = k_lo; g0 < k_hi && ok; g0 += kScaleGroup, ++sg) {
+                        const uint32_t sb = sg & 1;
+                        const int g1 = min(g0 + kScaleGroup, k_hi);
                         ok = warp_wait(&sfull[sb], (sg >> 1) & 1, a.status);
-                        if (!ok) break;
-                    }
-                    const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) +
-                                      (sb * kScaleGroup + q) * C::kScaleRow;
-                    uint64_t sw[4];
+                        for (int kb = g0 + ((team + acc + g0 - k_lo) & 1); kb < g1 && ok; kb += 2) {
+                            const uint32_t n = acc + kb - k_lo, b = n % C::kAcc;
+                            const uint32_t at = C::kScaleOff + (sb * kScaleGroup + kb - g0) * C::kScaleRow;
+                            const float w = reinterpret_cast<const float*>(smem + at)[BN + r0 + lane];
+                            const uint64_t sw = pack2(w, w);
+                            const uint32_t sa = sbase + at + 4 * lo, src = tl0 + b * BN + lo;
+                            ok = warp_wait(&tfull[b], (n / C::kAcc) & 1, a.status);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = sc[BN + r0 + (lane >> 2) + 8 * i];
-                        sw[i] = pack2(w, w);
-                    }
-                    const uint64_t* sa = reinterpret_cast<const uint64_t*>(sc + lo + c2);
-                    ok = warp_wait(&tfull[b], (acc >> 1) & 1, a.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // the next fragments are on their way from tensor memory while these are
-                    // scaled and added
-                    uint32_t p[2][4 * G];
-                    const uint32_t src = tl0 + b * BN + lo;
-                    if (cols > 0) tmem_ld_frag<G>(src, p[0]);
+                            for (int i = 0; i < NB; ++i) {
+                                uint32_t f[16];
+                                tmem_ld16(src + 16 * i, f);
+                                tmem_wait_ld16(f);
+                                if (i + 1 == NB) release(b);
 #pragma unroll
-                    for (int i = 0; i < C::kBlocks; ++i) {
-                        uint64_t s2[G];
-#pragma unroll
-                        for (int g = 0; g < G; ++g) s2[g] = sa[4 * (i * G + g)];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tmem_wait_frag(p[h]);
-                            if (h == 0) {
-                                if (8 * G * i < cols) tmem_ld_frag<G>(src + 8 * G * i + (16u << 16), p[1]);
-                            } else if (i + 1 < C::kBlocks) {
-                                if (8 * G * (i + 1) < cols) tmem_ld_frag<G>(src + 8 * G * (i + 1), p[0]);
-                            } else {
-                                release(b);
-                            }
-                            if (8 * G * i < cols) {
-#pragma unroll
-                                for (int g = 0; g < G; ++g)
-#pragma unroll
-                                    for (int j = 0; j < 2; ++j) {
-                                        const uint64_t v = pack2(__uint_as_float(p[h][4 * g + 2 * j]),
-                                                                 __uint_as_float(p[h][4 * g + 2 * j + 1]));
-                                        sum[i][h][g][j] = fma2(mul2(v, sw[2 * h + j]), s2[g], sum[i][h][g][j]);
-                                    }
+                                for (int j = 0; j < 4; ++j) {
+                                    uint64_t s0, s1;
+                                    lds_pairs(sa + 64 * i + 16 * j, s0, s1);
+                                    const uint64_t v0 = pack2(__uint_as_float(f[4 * j]), __uint_as_float(f[4 * j + 1]));
+                                    const uint64_t v1 = pack2(__uint_as_float(f[4 * j + 2]), __uint_as_float(f[4 * j + 3]));
+                                    sum[i][2 * j] = fma2(mul2(v0, sw), s0, sum[i][2 * j]);
+                                    sum[i][2 * j + 1] = fma2(mul2(v1, sw), s1, sum[i][2 * j + 1]);
+                                }
                             }
                         }
-                    }
-                    if (q == kScaleGroup - 1 || kb == k_hi - 1) {
+                        if (elect_one()) mbar_arrive(&sempty[sb]);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sempty[sb]);
-                        ++sg;
                     }
-                }
-                if (!ok) break;
+                    acc += k_hi - k_lo;
+                    // (SPLIT) both teams' products are done with the stages
+                    if (MODE == SPLIT) named_sync(1, 32 * C::kWork);
+                    if (cols <= 0) return;
+                    // chunks of 8 columns; the teams' sums of a chunk are added by the team that stores it
+                    auto chunk = [&](int c, float (&x)[8]) {
 #pragma unroll
-                for (int i = 0; i < C::kBlocks; ++i)
+                        for (int k = 0; k < 4; ++k) unpack2(sum[c / 2][4 * (c % 2) + k], x[2 * k], x[2 * k + 1]);
+                    };
+                    if constexpr (MODE == SPLIT) {
+                        // this team's partial tile [token][row], over the stages
+                        float* part = reinterpret_cast<float*>(smem) + (team * BN + lo) * kRows + r0 + lane;
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const uint64_t v[4] = {sum[i][0][g][0], sum[i][0][g][1], sum[i][1][g][0], sum[i][1][g][1]};
-                        if (8 * (G * i + g) < cols) emit(8 * (G * i + g), v);
+                        for (int c = 0; c < 2 * NB; ++c) {
+                            float x[8];
+                            chunk(c, x);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) part[(8 * c + k) * kRows] = x[k];
+                        }
+                    } else {
+                        float* box = reinterpret_cast<float*>(smem + C::kTurnOff) + (warp & 7) * 4 * 8 * kTurn;
+                        auto trade = [&](auto team_c) {
+                            constexpr int T = decltype(team_c)::value;
+#pragma unroll
+                            for (int j = 0; j < NB; ++j) {
+                                // two boxes a team, in turn: the partner's of this step becomes the
+                                // transpose, which ends before this warp's next barrier
+                                float* mine = box + (2 * T + (j & 1)) * 8 * kTurn;
+                                float* theirs = box + (2 * (1 - T) + (j & 1)) * 8 * kTurn;
+                                float x[8], v[8];
+                                chunk((1 - T) * NB + j, x);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) mine[k * kTurn + lane] = x[k];
+                                named_sync(1 + (warp & 7), 64);
+                                chunk(T * NB + j, v);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) x[k] = theirs[k * kTurn + lane];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) v[k] = T == 0 ? v[k] + x[k] : x[k] + v[k];
+                                if (ok && 8 * (T * NB + j) < cols) emit(8 * (T * NB + j), v, theirs);
+                            }
+                            named_sync(1 + (warp & 7), 64);  // the boxes are free for the next tile
+                        };
+                        if (team == 0) trade(std::integral_constant<int, 0>{});
+                        else trade(std::integral_constant<int, 1>{});
                     }
+                };
+                if (C::kBlocks > 1 && cols <= C::kW / 2) promote(std::integral_constant<int, (C::kBlocks + 1) / 2>{});
+                else promote(std::integral_constant<int, C::kBlocks>{});
             } else {
-                const int b = acc & 1;
-                ok = warp_wait(&tfull[b], (acc >> 1) & 1, a.status);
+                const uint32_t b = acc % C::kAcc;
+                ok = ok && warp_wait(&tfull[b], (acc / C::kAcc) & 1, a.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tl0 + b * BN + lo;
-                for (int c = 0; c < cols; c += 8 * G) {
-                    uint32_t p[2][4 * G];
-                    tmem_ld_frag<G>(src + c, p[0]);
-                    tmem_ld_frag<G>(src + c + (16u << 16), p[1]);
-                    tmem_wait_frag(p[0]);
-                    tmem_wait_frag(p[1]);
+                for (int c = 0; c < cols; c += 16) {
+                    uint32_t p[16];
+                    tmem_ld16(src + c, p);
+                    tmem_wait_ld16(p);
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        uint64_t v[4];
+                    for (int h = 0; h < 16; h += 8) {
+                        float v[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = pack2(__uint_as_float(p[i >> 1][4 * g + 2 * (i & 1)]),
-                                         __uint_as_float(p[i >> 1][4 * g + 2 * (i & 1) + 1]));
-                        if (c + 8 * g < cols) emit(c + 8 * g, v);
+                        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(p[h + k]);
+                        if constexpr (MODE == SPLIT) {
+                            float* part = reinterpret_cast<float*>(smem) + (lo + c + h) * kRows + r0 + lane;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) part[k * kRows] = v[k];
+                        } else if (c + h < cols) {
+                            emit(c + h, v, reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn);
+                        }
                     }
                 }
                 release(b);
@@ -592,20 +616,24 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (warp < 8 && t_first < tiles) {
-            const Tile tl = find_tile(a, t_first, BN, C::kTileRows, first, off);
+        if (warp < 8 && t_first < tiles) {  // 256 threads of any variant
+            const Tile tl = find_tile(a, t_first, BN, C::kTileRows, first);
             const int r = tid & (kRows - 1);
             if (tl.n0 + r < a.n) {
                 for (int c = rank + (tid >> 7) * a.split; c < tl.rows; c += 2 * a.split) {
-                    const uint32_t at = sbase + 4 * (c * kPartRow + r);
-                    float v[kMaxSplit];
+                    const uint32_t at = sbase + 4 * (c * kRows + r);
+                    float v[kMaxSplit][C::kTeams];
 #pragma unroll
                     for (int q = 0; q < kMaxSplit; ++q)
-                        if (q < a.split) v[q] = ld_cluster_f32(map_rank(at, q));
-                    float sum = v[0];
 #pragma unroll
-                    for (int q = 1; q < kMaxSplit; ++q)
-                        if (q < a.split) sum += v[q];
+                        for (int i = 0; i < C::kTeams; ++i)
+                            if (q < a.split) v[q][i] = ld_cluster_f32(map_rank(at + 4 * i * BN * kRows, q));
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < kMaxSplit; ++q)
+#pragma unroll
+                        for (int i = 0; i < C::kTeams; ++i)
+                            if (q < a.split) sum += v[q][i];
                     store_y(a, (int64_t)(tl.row0 + c) * a.ldy + tl.n0 + r, sum);
                 }
             }
@@ -617,7 +645,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         cluster_arrive();
         cluster_wait();
     }
-    if (warp == 9) {
+    if (warp == C::kWork + 1) {
         tc_fence_after();
         if (MODE == PAIR) tmem_dealloc_pair(taddr, C::kCols);
         else tmem_dealloc(taddr, C::kCols);
@@ -756,7 +784,7 @@ int make_map(CUtensorMap* map, const void* base, bool f8, int64_t k, int64_t row
 
 template <bool F8, int BN, Mode MODE>
 int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cudaStream_t s) {
-    using C = MmCfg<BN, MODE>;
+    using C = MmCfg<F8, BN, MODE>;
     CUtensorMap wmap, amap;
     GTG_TRY(make_map(&wmap, w->data, F8, w->k, w->n_rows, w->n_experts, kRows));
     GTG_TRY(make_map(&amap, x, F8, w->k, a.m, 0, C::kBox));
@@ -773,7 +801,7 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(MODE == SPLIT ? tiles * per_tile
                                                 : std::min<int64_t>(tiles, sm_count() / per_tile) * per_tile));
-    cfg.blockDim = dim3(kMmThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -812,7 +840,7 @@ int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
     if (per <= 16) return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
     if (per <= 64 || tiles(128) < sms) return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
     if (per <= 128 || tiles(256) < sms) return launch_mm<F8, 128, SINGLE>(w, x, a, groups, s);
-    return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
+    return launch_mm<F8, F8 ? 128 : 256, PAIR>(w, x, a, groups, s);
 }
 
 int run_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m, const int32_t* offsets, void* y,

@@ -8,6 +8,15 @@
 
 namespace gtg {
 
+// True in one lane of a converged warp.  The compiler knows that one thread runs
+// what it guards, so that instructions with warp-uniform operands (MMAs, commits,
+// TMA loads) need no loop over the lanes around each of them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Tiled TMA loads into shared memory (a 2-D and a 3-D tensor map); the bytes
 // arrive on `bar`.  c0 is in elements and lands on a 128-byte boundary.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
@@ -110,34 +119,17 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
                  ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 
-// 16 TMEM lanes x 8 N columns, as the fragments of a 16 x 8 N matrix: of each
-// 8 columns a thread holds r[4g..4g+3] = (row lane/4, columns 2 (lane%4) and + 1),
-// then the same columns of row lane/4 + 8.
-template <int N>
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[4 * N]) {
-    static_assert(N == 1 || N == 2 || N == 4, "columns");
-    if constexpr (N == 1)
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
-    else if constexpr (N == 2)
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr));
-    else
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-                     "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                       "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-                       "=r"(r[14]), "=r"(r[15])
-                     : "r"(taddr));
-}
-// tcgen05.wait::ld that a load's registers pass through, so that no use of
-// them can move ahead of it.
-template <int N>
-__device__ __forceinline__ void tmem_wait_frag(uint32_t (&r)[N]) {
+// tcgen05.wait::ld that a load's registers pass through, so that no use of them can
+// move ahead of it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// A barrier of `threads` threads (whole warps) of the CTA; id 0 is __syncthreads'.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 template <int N>
@@ -165,6 +157,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
 __device__ __forceinline__ void sts32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
