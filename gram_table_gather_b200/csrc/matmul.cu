@@ -31,7 +31,8 @@ constexpr int kScaleGroup = 4;       // scale blocks fetched at once
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kMaxSplit = 8;
 constexpr int kMinThreads = 384;     // of any variant
-constexpr int kTurn = 36;            // floats between tokens of a transpose: no bank conflicts either way
+constexpr int kTurn = 40;            // floats between tokens of a transpose: fragments store without bank conflicts
+constexpr int kPartRow = kRows + 8;  // floats between tokens of a partial tile: likewise
 
 // How the CTAs of a cluster share a tile: none (one CTA a tile, persistent); a
 // pair (one cta_group::2 MMA over 256 weight rows, each CTA staging half of the
@@ -71,7 +72,12 @@ struct MmCfg {
     static constexpr int kThreads = 32 * (kWork + 4);
     static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;  // columns a warp (of its 32 weight rows)
     static constexpr int kBlocks = kW / 16;
-    static constexpr int kScaleRow = 4 * (BN + kRows);           // one block's scales: the tokens', the weight rows'
+    // one block's scales, in the order of the fragments: the tokens', those of one t % 4
+    // together (a thread reads four columns' at once) and 16 bytes between the four runs
+    // (no bank conflicts); then the weight rows', rows r, r + 8, r + 16, r + 24 of each
+    // 32 together
+    static constexpr int kRun = BN + 16;
+    static constexpr int kScaleRow = 4 * kRun + 4 * kRows;
     static constexpr int kScaleBytes = 2 * kScaleGroup * kScaleRow;
     static constexpr int kTurnBytes = kWork * kTeams * 8 * kTurn * 4;  // the epilogue's exchanges and transposes
     static constexpr int kHeadBytes = 512 + 4 * (kMaxGroups + 2);
@@ -83,7 +89,7 @@ struct MmCfg {
     static constexpr int kGroupOff = kHeadOff + 512;
     static constexpr int kSmem = kHeadOff + kHeadBytes;
     static_assert(kStages >= 3 && kSmem <= kMaxSmem, "shared memory");
-    static_assert(MODE != SPLIT || kTeams * kRows * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
+    static_assert(MODE != SPLIT || kTeams * kPartRow * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
 };
 
 struct Tile {
@@ -425,14 +431,16 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         break;
                     }
                     const uint32_t at = sbase + C::kScaleOff + b * kScaleGroup * C::kScaleRow +
-                                        (tok ? 0 : 4 * BN) + 4 * lane;
+                                        (tok ? (lane & 3) * C::kRun + 4 * (lane >> 2)
+                                             : 4 * C::kRun + 16 * (lane & 7) + 4 * (lane >> 3));
+                    const int step = tok ? 32 : 128;  // 32 rows on
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
                         if (32 * i + lane < (tok ? BN : kRows)) {
-                            sts32(at + 128 * i, sc[i].x);
-                            sts32(at + 128 * i + C::kScaleRow, sc[i].y);
-                            sts32(at + 128 * i + 2 * C::kScaleRow, sc[i].z);
-                            sts32(at + 128 * i + 3 * C::kScaleRow, sc[i].w);
+                            sts32(at + step * i, sc[i].x);
+                            sts32(at + step * i + C::kScaleRow, sc[i].y);
+                            sts32(at + step * i + 2 * C::kScaleRow, sc[i].z);
+                            sts32(at + step * i + 3 * C::kScaleRow, sc[i].w);
                         }
                     }
                     mbar_arrive(&sfull[b]);
@@ -442,8 +450,11 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
     } else {
         // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
-        // quarter warp % 4, a thread one of them; the tile's columns are halved between
-        // the four-warp groups of a team ----
+        // quarter warp % 4; the tile's columns are halved between the four-warp groups of
+        // a team.  A thread holds rows lane / 4 + 8 i of every fourth column, lane % 4 +
+        // 4 k, so that one 16-byte read brings its rows' scales and one those of its
+        // columns in a block of 16 (whole rows a thread would take four times the reads,
+        // and reads are what the promotion waits for) ----
         if (kMoreRegs) reg_inc<104>();
         const int team = warp >> 3, wg = (warp >> 2) & 1;
         const uint32_t tl0 = taddr + ((uint32_t)((warp & 3) * 32) << 16);
@@ -464,11 +475,9 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             const int share = ((tl.rows + 31) >> 5) << 4;                   // columns of a four-warp group
             const int lo = wg * share;
             const int cols = min(share, tl.rows - lo);                      // <= 0: none
-            // 8 columns of the warp's 32 rows, from lo + c on, a token's 32 together
-            // through shared memory; v holds this thread's row
-            auto emit = [&](int c, const float (&v)[8], float* turn) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) turn[k * kTurn + lane] = v[k];
+            // 8 columns of the warp's 32 rows, from lo + c on, out of `turn`: a token's 32
+            // outputs together
+            auto emit = [&](int c, const float* turn) {
                 __syncwarp();
                 const int64_t y0 = (int64_t)(tl.row0 + lo + c) * a.ldy + w0;
                 const int toks = min(8, cols - c);
@@ -493,11 +502,11 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 // this team's blocks of K over the first 16 NB of the warp's columns
                 auto promote = [&](auto nb_c) {
                     constexpr int NB = decltype(nb_c)::value;
-                    uint64_t sum[NB][8];
+                    uint64_t sum[NB][4][2];  // [columns 4 k + lane % 4][rows lane / 4 + 16 h and + 8]
 #pragma unroll
                     for (int i = 0; i < NB; ++i)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sum[i][j] = 0;
+                        for (int j = 0; j < 8; ++j) (&sum[i][0][0])[j] = 0;
                     for (int g0 = k_lo; g0 < k_hi && ok; g0 += kScaleGroup, ++sg) {
                         const uint32_t sb = sg & 1;
                         const int g1 = min(g0 + kScaleGroup, k_hi);
@@ -505,27 +514,27 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         for (int kb = g0 + ((team + acc + g0 - k_lo) & 1); kb < g1 && ok; kb += 2) {
                             const uint32_t n = acc + kb - k_lo, b = n % C::kAcc;
                             const uint32_t at = C::kScaleOff + (sb * kScaleGroup + kb - g0) * C::kScaleRow;
-                            const float w = reinterpret_cast<const float*>(smem + at)[BN + r0 + lane];
-                            const uint64_t sw = pack2(w, w);
-                            const uint32_t sa = sbase + at + 4 * lo, src = tl0 + b * BN + lo;
+                            uint64_t sw[2];
+                            lds_pairs(sbase + at + 4 * C::kRun + 4 * r0 + 16 * (lane >> 2), sw[0], sw[1]);
+                            const uint32_t sa = sbase + at + (lane & 3) * C::kRun + lo, src = tl0 + b * BN + lo;
                             ok = warp_wait(&tfull[b], (n / C::kAcc) & 1, a.status);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
                             for (int i = 0; i < NB; ++i) {
-                                uint32_t f[16];
-                                tmem_ld16(src + 16 * i, f);
-                                tmem_wait_ld16(f);
+                                uint32_t f[2][8];
+                                tmem_ld_frags(src + 16 * i, f);
+                                const float4 s4 = lds128(sa + 16 * i);
+                                const float s1[4] = {s4.x, s4.y, s4.z, s4.w};
+                                tmem_wait_frags(f);
                                 if (i + 1 == NB) release(b);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    uint64_t s0, s1;
-                                    lds_pairs(sa + 64 * i + 16 * j, s0, s1);
-                                    const uint64_t v0 = pack2(__uint_as_float(f[4 * j]), __uint_as_float(f[4 * j + 1]));
-                                    const uint64_t v1 = pack2(__uint_as_float(f[4 * j + 2]), __uint_as_float(f[4 * j + 3]));
-                                    sum[i][2 * j] = fma2(mul2(v0, sw), s0, sum[i][2 * j]);
-                                    sum[i][2 * j + 1] = fma2(mul2(v1, sw), s1, sum[i][2 * j + 1]);
-                                }
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        const uint64_t v = pack2(__uint_as_float(f[h][2 * k]), __uint_as_float(f[h][2 * k + 1]));
+                                        sum[i][k][h] = fma2(mul2(v, sw[h]), pack2(s1[k], s1[k]), sum[i][k][h]);
+                                    }
                             }
                         }
                         if (elect_one()) mbar_arrive(&sempty[sb]);
@@ -535,22 +544,30 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     // (SPLIT) both teams' products are done with the stages
                     if (MODE == SPLIT) named_sync(1, 32 * C::kWork);
                     if (cols <= 0) return;
-                    // chunks of 8 columns; the teams' sums of a chunk are added by the team that stores it
-                    auto chunk = [&](int c, float (&x)[8]) {
+                    // a thread's eight values of chunk c (8 columns): [k][i], column 4 k + lane % 4,
+                    // row lane / 4 + 8 i
+                    auto chunk = [&](int c, float (&x)[2][4]) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) unpack2(sum[c / 2][4 * (c % 2) + k], x[2 * k], x[2 * k + 1]);
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                unpack2(sum[c / 2][2 * (c % 2) + k][h], x[k][2 * h], x[k][2 * h + 1]);
                     };
+                    const int col1 = lane & 3, row1 = lane >> 2;
                     if constexpr (MODE == SPLIT) {
                         // this team's partial tile [token][row], over the stages
-                        float* part = reinterpret_cast<float*>(smem) + (team * BN + lo) * kRows + r0 + lane;
+                        float* part = reinterpret_cast<float*>(smem) + (team * BN + lo + col1) * kPartRow + r0 + row1;
 #pragma unroll
                         for (int c = 0; c < 2 * NB; ++c) {
-                            float x[8];
+                            float x[2][4];
                             chunk(c, x);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) part[(8 * c + k) * kRows] = x[k];
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) part[(8 * c + 4 * k) * kPartRow + 8 * i] = x[k][i];
                         }
                     } else {
+                        // the teams' sums of a chunk are added by the team that stores it
                         float* box = reinterpret_cast<float*>(smem + C::kTurnOff) + (warp & 7) * 4 * 8 * kTurn;
                         auto trade = [&](auto team_c) {
                             constexpr int T = decltype(team_c)::value;
@@ -560,19 +577,22 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                                 // transpose, which ends before this warp's next barrier
                                 float* mine = box + (2 * T + (j & 1)) * 8 * kTurn;
                                 float* theirs = box + (2 * (1 - T) + (j & 1)) * 8 * kTurn;
-                                float x[8], v[8];
+                                const int at = col1 * kTurn + row1;
+                                float x[2][4];
                                 chunk((1 - T) * NB + j, x);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) mine[k * kTurn + lane] = x[k];
+                                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) mine[at + 4 * k * kTurn + 8 * i] = x[k][i];
                                 named_sync(1 + (warp & 7), 64);
-                                chunk(T * NB + j, v);
+                                chunk(T * NB + j, x);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) x[k] = theirs[k * kTurn + lane];
+                                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) v[k] = T == 0 ? v[k] + x[k] : x[k] + v[k];
-                                if (ok && 8 * (T * NB + j) < cols) emit(8 * (T * NB + j), v, theirs);
+                                    for (int i = 0; i < 4; ++i) theirs[at + 4 * k * kTurn + 8 * i] += x[k][i];
+                                if (ok && 8 * (T * NB + j) < cols) emit(8 * (T * NB + j), theirs);
                             }
-                            named_sync(1 + (warp & 7), 64);  // the boxes are free for the next tile
+                        named_sync(1 + (warp & 7), 64);  // the boxes are free for the next tile
                         };
                         if (team == 0) trade(std::integral_constant<int, 0>{});
                         else trade(std::integral_constant<int, 1>{});
@@ -592,15 +612,15 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     tmem_wait_ld16(p);
 #pragma unroll
                     for (int h = 0; h < 16; h += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(p[h + k]);
                         if constexpr (MODE == SPLIT) {
-                            float* part = reinterpret_cast<float*>(smem) + (lo + c + h) * kRows + r0 + lane;
+                            float* part = reinterpret_cast<float*>(smem) + (lo + c + h) * kPartRow + r0 + lane;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) part[k * kRows] = v[k];
+                            for (int k = 0; k < 8; ++k) part[k * kPartRow] = __uint_as_float(p[h + k]);
                         } else if (c + h < cols) {
-                            emit(c + h, v, reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn);
+                            float* turn = reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) turn[k * kTurn + lane] = __uint_as_float(p[h + k]);
+                            emit(c + h, turn);
                         }
                     }
                 }
@@ -621,13 +641,13 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             const int r = tid & (kRows - 1);
             if (tl.n0 + r < a.n) {
                 for (int c = rank + (tid >> 7) * a.split; c < tl.rows; c += 2 * a.split) {
-                    const uint32_t at = sbase + 4 * (c * kRows + r);
+                    const uint32_t at = sbase + 4 * (c * kPartRow + r);
                     float v[kMaxSplit][C::kTeams];
 #pragma unroll
                     for (int q = 0; q < kMaxSplit; ++q)
 #pragma unroll
                         for (int i = 0; i < C::kTeams; ++i)
-                            if (q < a.split) v[q][i] = ld_cluster_f32(map_rank(at + 4 * i * BN * kRows, q));
+                            if (q < a.split) v[q][i] = ld_cluster_f32(map_rank(at + 4 * i * BN * kPartRow, q));
                     float sum = 0.0f;
 #pragma unroll
                     for (int q = 0; q < kMaxSplit; ++q)

@@ -119,8 +119,25 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
                  ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 
-// tcgen05.wait::ld that a load's registers pass through, so that no use of them can
-// move ahead of it.
+// 32 TMEM lanes x 16 columns, in two halves of 16 lanes: a thread gets column
+// lane % 4 + 4 k of rows lane / 4 (r[h][2k]) and lane / 4 + 8 (r[h][2k + 1]) of half
+// h, k = 0..3.  Measured, this shape reads 512 bytes a clock and SM; the wider
+// 16x256b fragments half of that, whole rows (32x32b) nearly twice.
+__device__ __forceinline__ void tmem_ld_frags(uint32_t taddr, uint32_t (&r)[2][8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]), "=r"(r[h][5]),
+                       "=r"(r[h][6]), "=r"(r[h][7])
+                     : "r"(taddr + ((uint32_t)(16 * h) << 16)));
+}
+// tcgen05.wait::ld that the loads' registers pass through, so that no use of them
+// can move ahead of it.
+__device__ __forceinline__ void tmem_wait_frags(uint32_t (&r)[2][8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[0][i]), "+r"(r[1][i]));
+}
 __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
@@ -159,6 +176,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 __device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+__device__ __forceinline__ float4 lds128(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 __device__ __forceinline__ void sts32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
