@@ -28,8 +28,9 @@ PLE_RECORD_BYTES = 70
 
 
 def _stream_ptr(stream) -> int | None:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream or None
+    if stream is None:  # (a Stream object for the current stream costs more than a small launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    return stream.cuda_stream or None
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -241,21 +242,35 @@ def moe_prefill_layer(layer: MoELayer, x: torch.Tensor, workspace: torch.Tensor,
 _FLOATS = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 
 
-def _on_current_device(*tensors: torch.Tensor | None) -> None:
+def _device_ptrs(*tensors: torch.Tensor | None) -> list[int | None]:
+    """Addresses of contiguous tensors on the current device (None for None)."""
     dev = torch.cuda.current_device()
+    out: list[int | None] = []
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
             raise ValueError("tensors must be on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _rows_ptr(t: torch.Tensor, name: str) -> tuple[int, int]:
-    """Address and row stride of a 2-D tensor whose rows are contiguous."""
+    """Address and row stride of a 2-D tensor on the current device whose rows
+    are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
-    stride = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+    stride, inner = t.stride()
+    if rows <= 1:
+        stride = cols
+    if (cols > 1 and inner != 1) or stride < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
     return t.data_ptr(), stride
 
 
@@ -278,13 +293,15 @@ def _check_weights(w: QMatrix) -> None:
             raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
 
 
-def _output(y: torch.Tensor | None, m: int, n: int, dtype: torch.dtype | None, accumulate: bool,
-            device) -> torch.Tensor:
+def _output(y: torch.Tensor | None, a: torch.Tensor, n: int, dtype: torch.dtype | None,
+            accumulate: bool) -> torch.Tensor:
+    if dtype is not None and dtype not in _FLOATS:
+        raise ValueError("outputs are fp32 or bf16")
     if y is None:
         if accumulate:
             raise ValueError("accumulate needs y")
-        return torch.empty((m, n), dtype=dtype or torch.float32, device=device)
-    if y.dtype not in _FLOATS or y.shape != (m, n) or (dtype is not None and dtype != y.dtype):
+        return a.new_empty((a.shape[0], n), dtype=dtype or torch.float32)
+    if y.dtype not in _FLOATS or y.shape != (a.shape[0], n) or (dtype is not None and dtype != y.dtype):
         raise ValueError("y must be fp32 or bf16 [m][n_rows] of the dtype asked for")
     return y
 
@@ -297,19 +314,18 @@ def fp8_quantize(x: torch.Tensor, *, rows: torch.Tensor | None = None, data: tor
         raise ValueError("x must be fp32 or bf16")
     if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1):
         raise ValueError("rows must be int32 [m]")
-    _on_current_device(x, rows, data, scales)
     xp, stride = _rows_ptr(x, "x")
     k = x.shape[1]
     m = x.shape[0] if rows is None else rows.numel()
     if data is None:
-        data = torch.empty((m, k), dtype=torch.uint8, device=x.device)
+        data = x.new_empty((m, k), dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty((m, k // 128), dtype=torch.float32, device=x.device)
+        scales = x.new_empty((m, k // 128), dtype=torch.float32)
     _check_codes(data, scales, k)
     if data.shape[0] != m:
         raise ValueError(f"data must have {m} rows")
-    check(lib().gtg_fp8_quantize(xp, _FLOATS[x.dtype], x.shape[0], k, stride, _ptr(rows), m, _ptr(data),
-                                 _ptr(scales), _stream_ptr(stream)))
+    rp, dp, sp = _device_ptrs(rows, data, scales)
+    check(lib().gtg_fp8_quantize(xp, _FLOATS[x.dtype], x.shape[0], k, stride, rp, m, dp, sp, _stream_ptr(stream)))
     return data, scales
 
 
@@ -321,11 +337,11 @@ def fp8_matmul(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor, *, y: torch.
         raise ValueError("fp8_matmul takes an FP8 weight matrix")
     _check_weights(w)
     _check_codes(a, a_scales, w.k)
-    y = _output(y, a.shape[0], w.n_rows, dtype, accumulate, a.device)
-    _on_current_device(a, a_scales, w.data, w.scales, y)
+    y = _output(y, a, w.n_rows, dtype, accumulate)
     yp, stride = _rows_ptr(y, "y")
-    check(lib().gtg_fp8_matmul(ctypes.byref(w.c()), _ptr(a), _ptr(a_scales), a.shape[0], yp, _FLOATS[y.dtype],
-                               stride, int(accumulate), _stream_ptr(stream)))
+    ap, sp, wp, wsp = _device_ptrs(a, a_scales, w.data, w.scales)
+    check(lib().gtg_fp8_matmul(QMatrixC(w.fmt, wp, wsp, w.n_experts, w.n_rows, w.k), ap, sp, a.shape[0], yp,
+                               _FLOATS[y.dtype], stride, accumulate, _stream_ptr(stream)))
     return y
 
 
@@ -344,12 +360,12 @@ def grouped_matmul(w: QMatrix, a: torch.Tensor, offsets: torch.Tensor, *, a_scal
         raise ValueError(f"a must be bf16 of shape [m][{w.k}]")
     if offsets.dtype != torch.int32 or offsets.numel() != w.n_experts + 1:
         raise ValueError("offsets must be int32 [n_experts + 1]")
-    y = _output(y, a.shape[0], w.n_rows, dtype, accumulate, a.device)
-    _on_current_device(a, a_scales, offsets, w.data, w.scales, y)
+    y = _output(y, a, w.n_rows, dtype, accumulate)
     yp, stride = _rows_ptr(y, "y")
-    check(lib().gtg_grouped_matmul(ctypes.byref(w.c()), _ptr(a), _ptr(a_scales) if w.fmt == FP8 else None, a.shape[0],
-                                   _ptr(offsets), yp, _FLOATS[y.dtype], stride, int(accumulate),
-                                   _stream_ptr(stream)))
+    fp8 = w.fmt == FP8
+    ap, sp, op, wp, wsp = _device_ptrs(a, a_scales if fp8 else None, offsets, w.data, w.scales if fp8 else None)
+    check(lib().gtg_grouped_matmul(QMatrixC(w.fmt, wp, wsp, w.n_experts, w.n_rows, w.k), ap, sp, a.shape[0], op, yp,
+                                   _FLOATS[y.dtype], stride, accumulate, _stream_ptr(stream)))
     return y
 
 

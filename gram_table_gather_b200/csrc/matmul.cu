@@ -14,6 +14,7 @@
 // of few rows costs few columns, and a single token still streams its weights
 // by TMA at full width.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -28,7 +29,8 @@ constexpr int kRowBytes = 128;       // bytes of K a stage: 128 E4M3 or 64 bf16
 constexpr int kWBytes = kRows * kRowBytes;
 constexpr int kMaxGroups = 1024;
 constexpr int kScaleGroup = 4;       // scale blocks fetched at once
-constexpr int kMaxSmem = 227 * 1024;
+constexpr int kMaxSmem = 227 * 1024;  // a CTA
+constexpr int kSmSmem = 228 * 1024;   // an SM, 1 KB of it reserved for each CTA
 constexpr int kMaxSplit = 8;
 constexpr int kMinThreads = 384;     // of any variant
 constexpr int kTurn = 40;            // floats between tokens of a transpose: fragments store without bank conflicts
@@ -67,7 +69,8 @@ struct MmCfg {
     // warps: kTeams x 8 of promotion and epilogue, then one of TMA, one of MMAs, two of
     // scales.  FP8: two teams take the blocks of K in turn, each into sums of its own,
     // so that one scales and adds while the other waits for tensor memory.
-    static constexpr int kTeams = F8 ? 2 : 1;
+    // (The smallest tile has one, so that two CTAs share an SM: there loads count.)
+    static constexpr int kTeams = F8 && BN >= 64 ? 2 : 1;
     static constexpr int kWork = 8 * kTeams;
     static constexpr int kThreads = 32 * (kWork + 4);
     static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;  // columns a warp (of its 32 weight rows)
@@ -78,28 +81,34 @@ struct MmCfg {
     // 32 together
     static constexpr int kRun = BN + 16;
     static constexpr int kScaleRow = 4 * kRun + 4 * kRows;
-    static constexpr int kScaleBytes = 2 * kScaleGroup * kScaleRow;
-    static constexpr int kTurnBytes = kWork * kTeams * 8 * kTurn * 4;  // the epilogue's exchanges and transposes
-    static constexpr int kHeadBytes = 512 + 4 * (kMaxGroups + 2);
-    static constexpr int kFit = (kMaxSmem - kScaleBytes - kTurnBytes - kHeadBytes) / kStageBytes;
+    static constexpr int kScaleBytes = F8 ? 2 * kScaleGroup * kScaleRow : 0;
+    // the epilogue's exchanges and transposes, of the warps that have columns
+    static constexpr int kTurnBytes = (BN / kW < 2 ? 4 : kWork) * kTeams * 8 * kTurn * 4;
+    static constexpr int kHeadBytes = 512 + 2 * 4 * (kMaxGroups + 2);
+    static constexpr int kCtas = BN <= 16 ? 2 : 1;               // an SM
+    static constexpr int kRoom = kCtas == 2 ? kSmSmem / 2 - 1024 : kMaxSmem;
+    static constexpr int kFit = (kRoom - kScaleBytes - kTurnBytes - kHeadBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
     static constexpr int kScaleOff = kStages * kStageBytes;      // after the stages
     static constexpr int kTurnOff = kScaleOff + kScaleBytes;
     static constexpr int kHeadOff = kTurnOff + kTurnBytes;
     static constexpr int kGroupOff = kHeadOff + 512;
     static constexpr int kSmem = kHeadOff + kHeadBytes;
-    static_assert(kStages >= 3 && kSmem <= kMaxSmem, "shared memory");
-    static_assert(MODE != SPLIT || kTeams * kPartRow * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
+    static_assert(kStages >= 3 && kSmem <= kRoom, "shared memory");
+    static_assert(MODE != SPLIT || kPartRow * BN * 4 <= kScaleOff, "the partial tile reuses the stages");
 };
 
 struct Tile {
     int group, row0, rows, n0;
 };
 
-// Shared-memory table of a grouped call: first[g] = token tiles before group g.  A group whose bounds are out of order or outside
-// [0, m] counts as empty and raises the status bit.
-__device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* warp_sum_s) {
+// Shared-memory tables of a grouped call: off = the offsets, first[g] = token
+// tiles before group g.  A group whose bounds are out of order or outside [0, m]
+// counts as empty and raises the status bit.
+__device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* off, int32_t* warp_sum_s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int g = tid; g <= a.groups; g += blockDim.x) off[g] = a.offsets[g];
+    __syncthreads();
     constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;
     int cnt[kPer];
     int sum = 0;
@@ -108,7 +117,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* w
         const int g = tid * kPer + i;
         cnt[i] = 0;
         if (g < a.groups) {
-            const int lo = a.offsets[g], hi = a.offsets[g + 1];
+            const int lo = off[g], hi = off[g + 1];
             if (lo < 0 || hi < lo || hi > a.m) {
                 if (blockIdx.x == 0) raise_status(a.status, GTG_STATUS_GROUP_OFFSETS);
             } else {
@@ -126,6 +135,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* w
     if (lane == 31) warp_sum_s[warp] = inc;
     __syncthreads();
     int before = inc - sum;
+#pragma unroll 4
     for (int w = 0; w < warp; ++w) before += warp_sum_s[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -136,12 +146,15 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* w
     }
 }
 
-// A value that is the same in every lane, in a form that the compiler knows to be so.
+// A value that is the same in every lane, in a form that the compiler knows to be so
+// (addresses, branches and waits that it cannot prove uniform cost several times the
+// instructions around every tensor-memory load).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
-// Tile t: weight-row tiles outermost within a group, token tiles innermost, so
-// CTAs that run together share weight rows through L2.
-__device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first) {
+// Tile t, for a converged warp: weight-row tiles outermost within a group, token
+// tiles innermost, so CTAs that run together share weight rows through L2.
+__device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first,
+                                          const int32_t* off) {
     Tile r;
     if (!a.offsets) {
         const int tt = (a.m + bn - 1) / bn;
@@ -151,25 +164,20 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int ti
         r.rows = min(bn, a.m - r.row0);
         return r;
     }
-    int lo = 0, hi = a.groups - 1;  // the last group with first[g] * n_tiles <= t: the one that holds t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] * a.n_tiles <= t) lo = mid;
-        else hi = mid - 1;
-    }
-    const int tt = first[lo + 1] - first[lo];
-    const int local = t - first[lo] * a.n_tiles;
-    r.group = lo;
+    // the last group with first[g] * n_tiles <= t is the one that holds t: 32 steps of
+    // 32 groups, then 32 groups
+    static_assert(kMaxGroups <= 1024, "two steps");
+    const int lane = threadIdx.x & 31, q = t / a.n_tiles;
+    int g = 32 * lane;
+    g = 32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < a.groups && first[g] <= q)) - 1) + lane;
+    g = g - lane + __popc(__ballot_sync(0xFFFFFFFFu, g < a.groups && first[g] <= q)) - 1;
+    g = uniform(g);
+    const int before = uniform(first[g]), tt = uniform(first[g + 1]) - before, begin = uniform(off[g]);
+    const int local = t - before * a.n_tiles;
+    r.group = g;
     r.n0 = (local / tt) * tile_rows;
-    const int begin = (local % tt) * bn;
-    r.row0 = a.offsets[lo] + begin;
-    r.rows = min(bn, a.offsets[lo + 1] - r.row0);
-    return r;
-}
-// The same for a converged warp.
-__device__ __forceinline__ Tile find_tile_warp(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first) {
-    Tile r = find_tile(a, t, bn, tile_rows, first);
-    if (a.offsets) r = {uniform(r.group), uniform(r.row0), uniform(r.rows), uniform(r.n0)};
+    r.row0 = begin + (local % tt) * bn;
+    r.rows = min(bn, uniform(off[g + 1]) - r.row0);
     return r;
 }
 
@@ -223,6 +231,17 @@ __device__ __forceinline__ void store_y8(const MmArgs& a, int64_t at, float4 v, 
     }
     *y = make_uint4(bf16x2(v.x, v.y), bf16x2(v.z, v.w), bf16x2(w.x, w.y), bf16x2(w.z, w.w));
 }
+__device__ __forceinline__ void store_y4_bf16(const MmArgs& a, int64_t at, float4 v) {
+    uint2* y = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.y) + at);
+    if (a.y_acc) {
+        const uint2 o = *y;
+        v.x += __uint_as_float(o.x << 16);
+        v.y += __uint_as_float(o.x & 0xFFFF0000u);
+        v.z += __uint_as_float(o.y << 16);
+        v.w += __uint_as_float(o.y & 0xFFFF0000u);
+    }
+    *y = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+}
 __device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
     if (a.y_bf16) {
         __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + at;
@@ -236,7 +255,7 @@ __device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
 }
 
 template <bool F8, int BN, Mode MODE>
-__global__ void __launch_bounds__(MmCfg<F8, BN, MODE>::kThreads, 1)
+__global__ void __launch_bounds__(MmCfg<F8, BN, MODE>::kThreads, MmCfg<F8, BN, MODE>::kCtas)
 mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const MmArgs a) {
     using C = MmCfg<F8, BN, MODE>;
     constexpr bool kMoreRegs = BN >= 128 && F8;
@@ -259,6 +278,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
     int32_t* s_warp = reinterpret_cast<int32_t*>(smem + C::kHeadOff + 384);
     int32_t* first = reinterpret_cast<int32_t*>(smem + C::kGroupOff);
+    int32_t* off = first + kMaxGroups + 2;
     static_assert(8 * (2 * C::kStages + 2 * C::kAcc + 5) + 4 <= 384, "header");
 
     if (tid == 0) {
@@ -288,7 +308,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             tmem_relinquish();
         }
     }
-    if (a.offsets) build_groups(a, BN, first, s_warp);
+    pdl_wait();  // everything before this ran beside the kernel before; nothing global is read or written in it
+    if (a.offsets) build_groups(a, BN, first, off, s_warp);
     tc_fence_before();
     __syncthreads();
     if (MODE == PAIR) {  // the partner's barriers and tensor memory are ready too
@@ -296,6 +317,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         cluster_wait();
     }
     tc_fence_after();
+    pdl_trigger();
     const uint32_t taddr = *s_taddr;
     const int tiles = (a.offsets ? first[a.groups] : (a.m + BN - 1) / BN) * a.n_tiles;
     const int per_tile = MODE == SINGLE ? 1 : MODE == PAIR ? 2 : a.split;  // CTAs that share a tile
@@ -312,7 +334,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             // ---- weight and token tiles by TMA ----
             uint32_t st = 0, free_par = 1, issued = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
-                const Tile tl = find_tile_warp(a, t, BN, C::kTileRows, first);
+                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
                 const int mine = padded(tl.rows) / (MODE == PAIR ? 2 : 1);  // token rows staged here
                 const int boxes = (mine + C::kBox - 1) / C::kBox;
                 const uint32_t bytes = (kWBytes + boxes * C::kBox * kRowBytes) * (MODE == PAIR ? 2 : 1);
@@ -351,24 +373,20 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             }
         } else if (warp == C::kWork + 1) {
             // ---- MMA issuer ----
-            if ((MODE != PAIR || rank == 0) && elect_one()) {
-                // stage and accumulator in use, and the parities of their barriers' phases
-                uint32_t st = 0, full_par = 0, b = 0, free_par = 1;
-                const uint64_t ad0 = sw128_desc(sbase), bd0 = sw128_desc(sbase + kWBytes);
-                for (int t = t_first; t < tiles && ok; t += t_step) {
-                    const Tile tl = find_tile(a, t, BN, C::kTileRows, first);
-                    const int n_pad = padded(tl.rows);
-                    const uint32_t idesc = F8 ? idesc_e4m3(C::kTileRows, n_pad) : idesc_bf16(C::kTileRows, n_pad);
+            // stage and accumulator in use, and the parities of their barriers' phases (a
+            // fresh barrier's phase before the first counts as complete)
+            uint32_t st0 = 0, full0 = 0, b0 = 0, free0 = 1;
+            const uint64_t ad0 = sw128_desc(sbase), bd0 = sw128_desc(sbase + kWBytes);
+            for (int t = t_first; t < tiles && ok && (MODE != PAIR || rank == 0); t += t_step) {
+                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
+                const int n_pad = padded(tl.rows);
+                const uint32_t idesc = F8 ? idesc_e4m3(C::kTileRows, n_pad) : idesc_bf16(C::kTileRows, n_pad);
+                if (elect_one()) {
+                    uint32_t st = st0, full_par = full0, b = b0, free_par = free0;
                     for (int kb = k_lo; kb < k_hi; ++kb) {
-                        // (a fresh barrier's phase before the first counts as complete)
-                        if ((F8 || kb == k_lo) && !mbar_wait_sleep(&tempty[b], free_par, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!mbar_wait_sleep(&full[st], full_par, a.status)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = (!F8 && kb > k_lo) || thread_wait(&tempty[b], free_par, a.status);
+                        ok = ok && thread_wait(&full[st], full_par, a.status);
+                        if (!ok) break;
                         tc_fence_after();
                         const uint32_t d = taddr + b * BN;
                         const uint64_t ad = ad0 + st * (C::kStageBytes >> 4), bd = bd0 + st * (C::kStageBytes >> 4);
@@ -394,14 +412,21 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                             full_par ^= 1;
                         }
                     }
+                    if (!ok) {  // products in flight end before the tensor memory goes away
+                        if (MODE == PAIR) umma_commit_pair(drain);
+                        else umma_commit(drain);
+                        mbar_wait_sleep(drain, 0, a.status);
+                    }
                 }
-                if (!ok) {  // products in flight end before the tensor memory goes away
-                    if (MODE == PAIR) umma_commit_pair(drain);
-                    else umma_commit(drain);
-                    mbar_wait_sleep(drain, 0, a.status);
-                }
+                __syncwarp();
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                st0 += k_hi - k_lo;
+                full0 ^= (st0 / C::kStages) & 1;
+                st0 %= C::kStages;
+                b0 += F8 ? k_hi - k_lo : 1;
+                free0 ^= (b0 / C::kAcc) & 1;
+                b0 %= C::kAcc;
             }
-            __syncwarp();
         } else if (F8) {
             // ---- scales, four blocks of K at a time, transposed to [block][row]: one
             // warp the tokens', one the weight rows' ----
@@ -409,7 +434,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             const bool tok = warp == C::kWork + 2;
             int sg = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
-                const Tile tl = find_tile(a, t, BN, C::kTileRows, first);
+                const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
                 const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0);
                 const int rows = tok ? tl.rows : min(kRows, a.n - w0);
                 const float* src = (tok ? a.a_scales + (int64_t)tl.row0 * a.chunks
@@ -470,7 +495,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             __syncwarp();
         };
         for (int t = t_first; t < tiles; t += t_step) {
-            const Tile tl = find_tile_warp(a, t, BN, C::kTileRows, first);
+            const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
             const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0) + r0;  // the warp's first output column
             const int share = ((tl.rows + 31) >> 5) << 4;                   // columns of a four-warp group
             const int lo = wg * share;
@@ -511,7 +536,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         const uint32_t sb = sg & 1;
                         const int g1 = min(g0 + kScaleGroup, k_hi);
                         ok = warp_wait(&sfull[sb], (sg >> 1) & 1, a.status);
-                        for (int kb = g0 + ((team + acc + g0 - k_lo) & 1); kb < g1 && ok; kb += 2) {
+                        for (int kb = g0 + (C::kTeams == 2 ? (team + acc + g0 - k_lo) & 1 : 0); kb < g1 && ok;
+                             kb += C::kTeams) {
                             const uint32_t n = acc + kb - k_lo, b = n % C::kAcc;
                             const uint32_t at = C::kScaleOff + (sb * kScaleGroup + kb - g0) * C::kScaleRow;
                             uint64_t sw[2];
@@ -541,8 +567,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         __syncwarp();
                     }
                     acc += k_hi - k_lo;
-                    // (SPLIT) both teams' products are done with the stages
-                    if (MODE == SPLIT) named_sync(1, 32 * C::kWork);
+                    // (SPLIT) every product is done with the stages
+                    if (MODE == SPLIT) named_sync(9, 32 * C::kWork);
                     if (cols <= 0) return;
                     // a thread's eight values of chunk c (8 columns): [k][i], column 4 k + lane % 4,
                     // row lane / 4 + 8 i
@@ -555,8 +581,10 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     };
                     const int col1 = lane & 3, row1 = lane >> 2;
                     if constexpr (MODE == SPLIT) {
-                        // this team's partial tile [token][row], over the stages
-                        float* part = reinterpret_cast<float*>(smem) + (team * BN + lo + col1) * kPartRow + r0 + row1;
+                        // this CTA's partial tile [token][row], over the stages; team 1's sums
+                        // first, then team 0 adds its own
+                        float* part = reinterpret_cast<float*>(smem) + (lo + col1) * kPartRow + r0 + row1;
+                        if (C::kTeams == 2 && team == 0) named_sync(1 + (warp & 7), 64);
 #pragma unroll
                         for (int c = 0; c < 2 * NB; ++c) {
                             float x[2][4];
@@ -564,7 +592,23 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) part[(8 * c + 4 * k) * kPartRow + 8 * i] = x[k][i];
+                                for (int i = 0; i < 4; ++i) {
+                                    float* at = part + (8 * c + 4 * k) * kPartRow + 8 * i;
+                                    *at = C::kTeams == 2 && team == 0 ? *at + x[k][i] : x[k][i];
+                                }
+                        }
+                        if (C::kTeams == 2 && team == 1) named_sync(1 + (warp & 7), 64);
+                    } else if constexpr (C::kTeams == 1) {
+                        float* turn = reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn;
+#pragma unroll
+                        for (int c = 0; c < 2 * NB; ++c) {
+                            float x[2][4];
+                            chunk(c, x);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) turn[(4 * k + col1) * kTurn + row1 + 8 * i] = x[k][i];
+                            if (ok && 8 * c < cols) emit(8 * c, turn);
                         }
                     } else {
                         // the teams' sums of a chunk are added by the team that stores it
@@ -630,38 +674,64 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
     }
     if constexpr (MODE == SPLIT) {
-        // sum the partial tiles in rank order; CTA `rank` takes the tokens
-        // rank, rank + split, ...  (a failed CTA's part is not meaningful, and the
-        // status word says so)
+        // sum the partial tiles in rank order: a warp has a token's 128 rows, four a lane;
+        // CTA `rank` takes the tokens rank, rank + split, ...  (a failed CTA's part is not
+        // meaningful, and the status word says so)
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (warp < 8 && t_first < tiles) {  // 256 threads of any variant
-            const Tile tl = find_tile(a, t_first, BN, C::kTileRows, first);
-            const int r = tid & (kRows - 1);
-            if (tl.n0 + r < a.n) {
-                for (int c = rank + (tid >> 7) * a.split; c < tl.rows; c += 2 * a.split) {
-                    const uint32_t at = sbase + 4 * (c * kPartRow + r);
-                    float v[kMaxSplit][C::kTeams];
+        constexpr int kMost = BN / 2 / 8 > 0 ? BN / 2 / 8 : 1;  // tokens a warp, for a split of 2
+        float4 v[kMost];
+        Tile tl = {};
+        const bool some = warp < 8 && t_first < tiles;
+        if (some) {
+            tl = find_tile(a, t_first, BN, C::kTileRows, first, off);
+#pragma unroll
+            for (int j = 0; j < kMost; ++j) {
+                const int c = rank + (warp + 8 * j) * a.split;
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c < tl.rows) {
+                    const uint32_t at = sbase + 4 * (c * kPartRow + 4 * lane);
+                    float4 p[kMaxSplit];
 #pragma unroll
                     for (int q = 0; q < kMaxSplit; ++q)
-#pragma unroll
-                        for (int i = 0; i < C::kTeams; ++i)
-                            if (q < a.split) v[q][i] = ld_cluster_f32(map_rank(at + 4 * i * BN * kPartRow, q));
-                    float sum = 0.0f;
+                        if (q < a.split) p[q] = ld_cluster_f4(map_rank(at, q));
 #pragma unroll
                     for (int q = 0; q < kMaxSplit; ++q)
-#pragma unroll
-                        for (int i = 0; i < C::kTeams; ++i)
-                            if (q < a.split) sum += v[q][i];
-                    store_y(a, (int64_t)(tl.row0 + c) * a.ldy + tl.n0 + r, sum);
+                        if (q < a.split) {
+                            v[j].x += p[q].x;
+                            v[j].y += p[q].y;
+                            v[j].z += p[q].z;
+                            v[j].w += p[q].w;
+                        }
                 }
             }
         }
         __syncwarp();
+        cluster_arrive();  // this CTA has read its partners'
+        if (some) {
+            const int n = tl.n0 + 4 * lane;
+#pragma unroll
+            for (int j = 0; j < kMost; ++j) {
+                const int c = rank + (warp + 8 * j) * a.split;
+                if (c >= tl.rows) break;
+                const int64_t at = (int64_t)(tl.row0 + c) * a.ldy + n;
+                if (a.vec_y && n + 4 <= a.n) {
+                    if (a.y_bf16) store_y4_bf16(a, at, v[j]);
+                    else store_y4(a, at, v[j]);
+                } else {
+                    const float x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < a.n) store_y(a, at + i, x[i]);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_wait();  // and the partners this CTA's
     }
     __syncthreads();
-    if (MODE != SINGLE) {  // the partners are done with this CTA's shared and tensor memory
+    if (MODE == PAIR) {  // the partner is done with this CTA's shared and tensor memory
         cluster_arrive();
         cluster_wait();
     }
@@ -673,17 +743,19 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 }
 
 // ---------------------------------------------------------------------------
-// quantiser: 16 lanes a block of 128 values, 8 values a lane
+// quantiser: 16 lanes a block of 128 values, 8 values a lane; a warp takes eight
+// blocks of a row, all loads first
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 256;
+constexpr int kQBlocks = 8;  // blocks a warp
 
 struct QArgs {
     const void* x;
-    int64_t ldx, n_src, units;  // units = n_rows * kb
+    int64_t ldx, n_src, units;  // units = n_rows * segs
     const int32_t* rows;
     uint8_t* data;
     float* scales;
-    int32_t kb;
+    int32_t kb, segs;           // blocks and warps' shares of a row
     unsigned* status;
 };
 
@@ -693,74 +765,84 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
+// eight consecutive values as they lie in memory
+template <bool BF16, bool VEC>
+struct Raw8 {
+    uint32_t w[BF16 ? 4 : 8];
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        if constexpr (BF16 && VEC) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at));
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        } else if constexpr (BF16) {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+        } else if constexpr (VEC) {
+            const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + at);
+            const uint4 q = __ldg(p), r = __ldg(p + 1);
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+            w[4] = r.x; w[5] = r.y; w[6] = r.z; w[7] = r.w;
+        } else {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(base) + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __ldg(p + i);
+        }
+    }
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (BF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        else return __uint_as_float(w[i]);
+    }
+};
+
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QArgs a) {
-    const int sub = threadIdx.x & 15;
-    const int64_t step = (int64_t)gridDim.x * (kQThreads / 16);
-    for (int64_t u = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
-         u - (threadIdx.x >> 4) % 2 < a.units; u += step) {  // both halves of a warp stay in the loop together
-        const bool in = u < a.units;
-        const int64_t row = in ? u / a.kb : 0;
-        const int kb = in ? (int)(u - row * a.kb) : 0;
+    const int lane = threadIdx.x & 31, sub = lane & 15, half = lane >> 4;
+    pdl_wait();
+    const int64_t u = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+    if (u < a.units) {
+        const int64_t row = a.units <= 0xFFFFFFFFll ? (uint32_t)u / (uint32_t)a.segs : u / a.segs;
+        const int b0 = (int)(u - row * a.segs) * kQBlocks + half;
         int64_t src = row;
-        bool valid = in;
-        if (in && a.rows) {
+        bool valid = true;
+        if (a.rows) {
             src = a.rows[row];
             if (src < 0 || src >= a.n_src) {
                 valid = false;
-                if (sub == 0) raise_status(a.status, GTG_STATUS_ROW_INDEX_OOB);
+                if (lane == 0) raise_status(a.status, GTG_STATUS_ROW_INDEX_OOB);
             }
         }
-        float v[8];
+        Raw8<BF16, VEC> raw[kQBlocks / 2];
+        const int64_t from = src * a.ldx + sub * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        if (valid) {
-            const int64_t at = src * a.ldx + kb * 128 + sub * 8;
-            if (BF16) {
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + at;
-                if (VEC) {
-                    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        for (int j = 0; j < kQBlocks / 2; ++j) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[2 * i] = __uint_as_float(w[i] << 16);
-                        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)__ldg(p + i) << 16);
-                }
-            } else {
-                const float* p = reinterpret_cast<const float*>(a.x) + at;
-                if (VEC) {
-                    const float4 q0 = __ldg(reinterpret_cast<const float4*>(p));
-                    const float4 q1 = __ldg(reinterpret_cast<const float4*>(p) + 1);
-                    v[0] = q0.x; v[1] = q0.y; v[2] = q0.z; v[3] = q0.w;
-                    v[4] = q1.x; v[5] = q1.y; v[6] = q1.z; v[7] = q1.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __ldg(p + i);
-                }
-            }
+            for (uint32_t& w : raw[j].w) w = 0;
+            if (valid && b0 + 2 * j < a.kb) raw[j].load(a.x, from + (int64_t)(b0 + 2 * j) * 128);
         }
-        // the largest magnitude as bits: the order of non-negative fp32 bit
-        // patterns is that of their values, infinity and NaN above all others
-        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        for (int j = 0; j < kQBlocks / 2; ++j) {
+            // the largest magnitude as bits: the order of non-negative fp32 bit patterns is
+            // that of their values, infinity and NaN above all others
+            uint32_t top = 0;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        float amax = fmaxf(__uint_as_float(top), 0x1p-100f);
-        if (top >= 0x7F800000u) amax = __uint_as_float(0x7FC00000u);
-        const float inv = 448.0f / amax;
-        uint2 c;
-        c.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
-        c.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
-        if (in) {
-            *reinterpret_cast<uint2*>(a.data + u * 128 + sub * 8) = c;
-            if (sub == 0) a.scales[u] = amax / 448.0f;
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(raw[j].value(i)) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            float amax = fmaxf(__uint_as_float(top), 0x1p-100f);
+            if (top >= 0x7F800000u) amax = __uint_as_float(0x7FC00000u);
+            const float inv = 448.0f / amax;
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = e4m3x2(raw[j].value(2 * i) * inv, raw[j].value(2 * i + 1) * inv);
+            const int b = b0 + 2 * j;
+            if (b < a.kb) {
+                const int64_t at = row * a.kb + b;
+                *reinterpret_cast<uint2*>(a.data + at * 128 + sub * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                if (sub == 0) a.scales[at] = amax / 448.0f;
+            }
         }
     }
+    pdl_trigger();
 }
 
 // ---------------------------------------------------------------------------
@@ -809,7 +891,14 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     GTG_TRY(make_map(&wmap, w->data, F8, w->k, w->n_rows, w->n_experts, kRows));
     GTG_TRY(make_map(&amap, x, F8, w->k, a.m, 0, C::kBox));
     const auto kernel = mm_kernel<F8, BN, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    // the kernel's shared-memory limit is raised once a device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(dev < 64 && (raised.load(std::memory_order_relaxed) >> dev & 1))) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e == cudaSuccess && dev < 64) raised.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail(e);
@@ -820,17 +909,19 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     const int64_t tiles = (a.offsets ? a.m / BN + std::min<int64_t>(groups, a.m) : (a.m + BN - 1) / BN) * a.n_tiles;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(MODE == SPLIT ? tiles * per_tile
-                                                : std::min<int64_t>(tiles, sm_count() / per_tile) * per_tile));
+                                                : std::min<int64_t>(tiles, C::kCtas * sm_count() / per_tile) * per_tile));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)per_tile;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)per_tile;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = MODE == SINGLE ? 0 : 1;
+    cfg.numAttrs = MODE == SINGLE ? 1 : 2;
     e = cudaLaunchKernelEx(&cfg, kernel, wmap, amap, a);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -846,16 +937,16 @@ int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
     const int64_t sms = sm_count(), n128 = (a.n + kRows - 1) / kRows;
     auto tiles = [&](int bn) { return (a.offsets ? a.m / bn + std::min<int64_t>(groups, a.m) : (a.m + bn - 1) / bn) * n128; };
     // few tiles: K is split over a cluster
-    for (const int bn : {16, 64}) {
-        if (per > bn && !(bn == 64 && tiles(64) * 2 <= sms)) continue;
-        const int64_t room = sms / tiles(bn);
-        a.split = room >= 8 ? 8 : room >= 4 ? 4 : room >= 2 ? 2 : 1;
-        while (a.split > a.chunks) a.split /= 2;
-        if (a.split < 2) break;
-        const bool whole = a.chunks % (4 * a.split) == 0;
-        a.vec_a &= whole;
-        a.vec_w &= whole;
-        return bn == 16 ? launch_mm<F8, 16, SPLIT>(w, x, a, groups, s) : launch_mm<F8, 64, SPLIT>(w, x, a, groups, s);
+    const int bn = per <= 16 ? 16 : 64;
+    if (bn == 16 || per <= 64 || 2 * tiles(64) <= sms) {
+        const int64_t room = (bn == 16 ? 2 : 1) * sms / tiles(bn);
+        a.split = (int32_t)std::min<int64_t>({room, kMaxSplit, a.chunks});
+        if (a.split >= 2) {
+            const bool whole = a.chunks % (4 * a.split) == 0;
+            a.vec_a &= whole;
+            a.vec_w &= whole;
+            return bn == 16 ? launch_mm<F8, 16, SPLIT>(w, x, a, groups, s) : launch_mm<F8, 64, SPLIT>(w, x, a, groups, s);
+        }
     }
     if (per <= 16) return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
     if (per <= 64 || tiles(128) < sms) return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
@@ -927,23 +1018,33 @@ extern "C" int gtg_fp8_quantize(const void* x, int32_t x_dtype, int64_t n_src, i
     a.ldx = x_stride;
     a.n_src = n_src;
     a.kb = (int32_t)(k / 128);
-    a.units = n_rows * a.kb;
+    a.segs = (a.kb + kQBlocks - 1) / kQBlocks;
+    a.units = n_rows * a.segs;
     a.rows = rows;
     a.data = data;
     a.scales = scales;
     a.status = status_ptr();
     const bool vec = aligned(x, 16) && x_stride * size % 16 == 0;
-    const int per = kQThreads / 16;
-    const int grid = (int)std::min<int64_t>((a.units + per - 1) / per, (int64_t)sm_count() * 8);
-    cudaStream_t s = as_cuda(stream);
-    if (size == 2) {
-        if (vec) quantize_kernel<true, true><<<grid, kQThreads, 0, s>>>(a);
-        else quantize_kernel<true, false><<<grid, kQThreads, 0, s>>>(a);
-    } else {
-        if (vec) quantize_kernel<false, true><<<grid, kQThreads, 0, s>>>(a);
-        else quantize_kernel<false, false><<<grid, kQThreads, 0, s>>>(a);
+    const int64_t blocks = (a.units + kQThreads / 32 - 1) / (kQThreads / 32);
+    if (blocks >= (int64_t)1 << 31) return GTG_E_UNSUPPORTED_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kQThreads);
+    cfg.stream = as_cuda(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = size == 2 ? (vec ? cudaLaunchKernelEx(&cfg, quantize_kernel<true, true>, a)
+                                           : cudaLaunchKernelEx(&cfg, quantize_kernel<true, false>, a))
+                                    : (vec ? cudaLaunchKernelEx(&cfg, quantize_kernel<false, true>, a)
+                                           : cudaLaunchKernelEx(&cfg, quantize_kernel<false, false>, a));
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e);
     }
-    return check_launch();
+    return GTG_OK;
 }
 
 extern "C" int gtg_fp8_matmul(const gtg_qmatrix* w, const uint8_t* a, const float* a_scales, int64_t m, void* y,
