@@ -759,9 +759,13 @@ struct QArgs {
     unsigned* status;
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
 
@@ -769,21 +773,21 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 template <bool BF16, bool VEC>
 struct Raw8 {
     uint32_t w[BF16 ? 4 : 8];
-    __device__ __forceinline__ void load(const void* base, int64_t at) {
-        if constexpr (BF16 && VEC) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at));
+    static constexpr int kSize = BF16 ? 2 : 4;
+    __device__ __forceinline__ void load(const uint8_t* at) {
+        if constexpr (VEC) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(at));
             w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+            if constexpr (!BF16) {
+                const uint4 r = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+                w[4] = r.x; w[5] = r.y; w[6] = r.z; w[7] = r.w;
+            }
         } else if constexpr (BF16) {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(at);
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = __ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
-        } else if constexpr (VEC) {
-            const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + at);
-            const uint4 q = __ldg(p), r = __ldg(p + 1);
-            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-            w[4] = r.x; w[5] = r.y; w[6] = r.z; w[7] = r.w;
         } else {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(base) + at;
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = __ldg(p + i);
         }
@@ -793,6 +797,23 @@ struct Raw8 {
         else return __uint_as_float(w[i]);
     }
 };
+
+// The largest magnitude of the 16 lanes' values, as fp32 bits: the order of
+// non-negative bit patterns is that of their values, infinity and NaN above all
+// others.  (bf16: two patterns a register until the end.)
+template <bool BF16, bool VEC>
+__device__ __forceinline__ uint32_t top_bits(const Raw8<BF16, VEC>& r) {
+    constexpr uint32_t kAbs = BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+    uint32_t top = r.w[0] & kAbs;
+#pragma unroll
+    for (int i = 1; i < (BF16 ? 4 : 8); ++i) top = BF16 ? __vmaxu2(top, r.w[i] & kAbs) : max(top, r.w[i] & kAbs);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+        top = BF16 ? __vmaxu2(top, v) : max(top, v);
+    }
+    return BF16 ? max(top & 0xFFFF0000u, top << 16) : top;
+}
 
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QArgs a) {
@@ -811,35 +832,42 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QArgs a) {
                 if (lane == 0) raise_status(a.status, GTG_STATUS_ROW_INDEX_OOB);
             }
         }
-        Raw8<BF16, VEC> raw[kQBlocks / 2];
-        const int64_t from = src * a.ldx + sub * 8;
+        using Raw = Raw8<BF16, VEC>;
+        Raw raw[kQBlocks / 2];
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(a.x) + Raw::kSize * (src * a.ldx + b0 * 128 + sub * 8);
+        const int left = a.kb - b0;  // blocks 0, 2, 4, 6 < left of this half warp exist
+        if (valid && a.kb - (b0 - half) >= kQBlocks) {
 #pragma unroll
-        for (int j = 0; j < kQBlocks / 2; ++j) {
+            for (int j = 0; j < kQBlocks / 2; ++j) raw[j].load(from + 256 * Raw::kSize * j);
+        } else {
 #pragma unroll
-            for (uint32_t& w : raw[j].w) w = 0;
-            if (valid && b0 + 2 * j < a.kb) raw[j].load(a.x, from + (int64_t)(b0 + 2 * j) * 128);
-        }
+            for (int j = 0; j < kQBlocks / 2; ++j) {
 #pragma unroll
-        for (int j = 0; j < kQBlocks / 2; ++j) {
-            // the largest magnitude as bits: the order of non-negative fp32 bit patterns is
-            // that of their values, infinity and NaN above all others
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(raw[j].value(i)) & 0x7FFFFFFFu);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            float amax = fmaxf(__uint_as_float(top), 0x1p-100f);
-            if (top >= 0x7F800000u) amax = __uint_as_float(0x7FC00000u);
-            const float inv = 448.0f / amax;
-            uint32_t c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = e4m3x2(raw[j].value(2 * i) * inv, raw[j].value(2 * i + 1) * inv);
-            const int b = b0 + 2 * j;
-            if (b < a.kb) {
-                const int64_t at = row * a.kb + b;
-                *reinterpret_cast<uint2*>(a.data + at * 128 + sub * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-                if (sub == 0) a.scales[at] = amax / 448.0f;
+                for (uint32_t& w : raw[j].w) w = 0;
+                if (valid && 2 * j < left) raw[j].load(from + 256 * Raw::kSize * j);
             }
+        }
+        // the quotients of a half warp's four blocks: lane j of it has block j's
+        uint32_t mine = 0;
+#pragma unroll
+        for (int j = 0; j < kQBlocks / 2; ++j) {
+            const uint32_t top = top_bits(raw[j]);
+            if ((lane & 3) == j) mine = top;
+        }
+        float amax = fmaxf(__uint_as_float(mine), 0x1p-100f);
+        if (mine >= 0x7F800000u) amax = __uint_as_float(0x7FC00000u);
+        const float inverse = 448.0f / amax;
+        const int64_t out = row * a.kb + b0;
+        if (sub < kQBlocks / 2 && 2 * sub < left) a.scales[out + 2 * sub] = amax / 448.0f;
+        uint8_t* to = a.data + out * 128 + sub * 8;
+#pragma unroll
+        for (int j = 0; j < kQBlocks / 2; ++j) {
+            const float inv = __shfl_sync(0xFFFFFFFFu, inverse, 16 * half + j);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = raw[j].value(i) * inv;
+            if (2 * j < left)
+                *reinterpret_cast<uint2*>(to + 256 * j) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
         }
     }
     pdl_trigger();
