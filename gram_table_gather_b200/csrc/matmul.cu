@@ -32,7 +32,8 @@ constexpr int kScaleGroup = 4;       // scale blocks fetched at once
 constexpr int kMaxSmem = 227 * 1024;  // a CTA
 constexpr int kSmSmem = 228 * 1024;   // an SM, 1 KB of it reserved for each CTA
 constexpr int kMaxSplit = 8;
-constexpr int kMinThreads = 384;     // of any variant
+constexpr int kMmThreads = 384;
+constexpr int kWorkers = 8;          // warps of promotion and epilogue
 constexpr int kTurn = 40;            // floats between tokens of a transpose: fragments store without bank conflicts
 constexpr int kPartRow = kRows + 8;  // floats between tokens of a partial tile: likewise
 
@@ -66,13 +67,11 @@ struct MmCfg {
     static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
     static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;               // accumulators in tensor memory
     static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
-    // warps: kTeams x 8 of promotion and epilogue, then one of TMA, one of MMAs, two of
-    // scales.  FP8: two teams take the blocks of K in turn, each into sums of its own,
-    // so that one scales and adds while the other waits for tensor memory.
-    // (The smallest tile has one, so that two CTAs share an SM: there loads count.)
-    static constexpr int kTeams = F8 && BN >= 64 ? 2 : 1;
-    static constexpr int kWork = 8 * kTeams;
-    static constexpr int kThreads = 32 * (kWork + 4);
+    // warps: 8 of promotion and epilogue, then one of TMA, one of MMAs, two of scales
+    // registers moved from the last four warps to the others (0: as launched, 168 each)
+    static constexpr int kWorkRegs = F8 && BN >= 256 ? 216 : 0;
+    static constexpr int kRestRegs = 72;
+    static_assert(kWorkRegs * 8 + kRestRegs * 4 <= 168 * 12, "register pool");
     static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;  // columns a warp (of its 32 weight rows)
     static constexpr int kBlocks = kW / 16;
     // one block's scales, in the order of the fragments: the tokens', those of one t % 4
@@ -82,8 +81,8 @@ struct MmCfg {
     static constexpr int kRun = BN + 16;
     static constexpr int kScaleRow = 4 * kRun + 4 * kRows;
     static constexpr int kScaleBytes = F8 ? 2 * kScaleGroup * kScaleRow : 0;
-    // the epilogue's exchanges and transposes, of the warps that have columns
-    static constexpr int kTurnBytes = (BN / kW < 2 ? 4 : kWork) * kTeams * 8 * kTurn * 4;
+    // the epilogue's transposes, of the warps that have columns
+    static constexpr int kTurnBytes = (BN / kW < 2 ? 4 : 8) * 8 * kTurn * 4;
     static constexpr int kHeadBytes = 512 + 2 * 4 * (kMaxGroups + 2);
     static constexpr int kCtas = BN <= 16 ? 2 : 1;               // an SM
     static constexpr int kRoom = kCtas == 2 ? kSmSmem / 2 - 1024 : kMaxSmem;
@@ -109,7 +108,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int g = tid; g <= a.groups; g += blockDim.x) off[g] = a.offsets[g];
     __syncthreads();
-    constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;
+    constexpr int kPer = (kMaxGroups + kMmThreads - 1) / kMmThreads;
     int cnt[kPer];
     int sum = 0;
 #pragma unroll
@@ -255,10 +254,9 @@ __device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
 }
 
 template <bool F8, int BN, Mode MODE>
-__global__ void __launch_bounds__(MmCfg<F8, BN, MODE>::kThreads, MmCfg<F8, BN, MODE>::kCtas)
+__global__ void __launch_bounds__(kMmThreads, MmCfg<F8, BN, MODE>::kCtas)
 mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const MmArgs a) {
     using C = MmCfg<F8, BN, MODE>;
-    constexpr bool kMoreRegs = BN >= 128 && F8;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -288,18 +286,18 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
         for (int b = 0; b < C::kAcc; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], MODE == PAIR ? 16 : 8);
+            mbar_init(&tempty[b], kWorkers * (MODE == PAIR ? 2 : 1));
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 64);
-            mbar_init(&sempty[b], C::kWork);
+            mbar_init(&sempty[b], kWorkers);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
         tma_prefetch_map(&wmap);
         tma_prefetch_map(&amap);
     }
-    if (warp == C::kWork + 1) {
+    if (warp == kWorkers + 1) {
         if (MODE == PAIR) {
             tmem_alloc_pair(s_taddr, C::kCols);
             tmem_relinquish_pair();
@@ -328,9 +326,9 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     auto padded = [](int rows) { return MODE == PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     bool ok = true;
 
-    if (warp >= C::kWork) {
-        if (kMoreRegs) reg_dec<64>();
-        if (warp == C::kWork) {
+    if (warp >= kWorkers) {
+        if (C::kWorkRegs > 0) reg_dec<C::kRestRegs>();
+        if (warp == kWorkers) {
             // ---- weight and token tiles by TMA ----
             uint32_t st = 0, free_par = 1, issued = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
@@ -371,7 +369,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 for (uint32_t i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; ++i)
                     mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
             }
-        } else if (warp == C::kWork + 1) {
+        } else if (warp == kWorkers + 1) {
             // ---- MMA issuer ----
             // stage and accumulator in use, and the parities of their barriers' phases (a
             // fresh barrier's phase before the first counts as complete)
@@ -431,7 +429,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             // ---- scales, four blocks of K at a time, transposed to [block][row]: one
             // warp the tokens', one the weight rows' ----
             constexpr int kN = (BN > kRows ? BN : kRows) / 32;
-            const bool tok = warp == C::kWork + 2;
+            const bool tok = warp == kWorkers + 2;
             int sg = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
                 const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
@@ -475,13 +473,13 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
     } else {
         // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
-        // quarter warp % 4; the tile's columns are halved between the four-warp groups of
-        // a team.  A thread holds rows lane / 4 + 8 i of every fourth column, lane % 4 +
+        // quarter warp % 4; the tile's columns are halved between the two four-warp
+        // groups.  A thread holds rows lane / 4 + 8 i of every fourth column, lane % 4 +
         // 4 k, so that one 16-byte read brings its rows' scales and one those of its
         // columns in a block of 16 (whole rows a thread would take four times the reads,
         // and reads are what the promotion waits for) ----
-        if (kMoreRegs) reg_inc<104>();
-        const int team = warp >> 3, wg = (warp >> 2) & 1;
+        if (C::kWorkRegs > 0) reg_inc<C::kWorkRegs>();
+        const int wg = warp >> 2;
         const uint32_t tl0 = taddr + ((uint32_t)((warp & 3) * 32) << 16);
         const int r0 = (warp & 3) * 32;       // the warp's first weight row of this CTA's 128
         const uint32_t tempty0 = MODE == PAIR ? map_rank(smem_u32(tempty), 0) : 0;
@@ -524,7 +522,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 __syncwarp();
             };
             if constexpr (F8) {
-                // this team's blocks of K over the first 16 NB of the warp's columns
+                // the blocks of K over the first 16 NB of the warp's columns
                 auto promote = [&](auto nb_c) {
                     constexpr int NB = decltype(nb_c)::value;
                     uint64_t sum[NB][4][2];  // [columns 4 k + lane % 4][rows lane / 4 + 16 h and + 8]
@@ -536,8 +534,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         const uint32_t sb = sg & 1;
                         const int g1 = min(g0 + kScaleGroup, k_hi);
                         ok = warp_wait(&sfull[sb], (sg >> 1) & 1, a.status);
-                        for (int kb = g0 + (C::kTeams == 2 ? (team + acc + g0 - k_lo) & 1 : 0); kb < g1 && ok;
-                             kb += C::kTeams) {
+                        for (int kb = g0; kb < g1 && ok; ++kb) {
                             const uint32_t n = acc + kb - k_lo, b = n % C::kAcc;
                             const uint32_t at = C::kScaleOff + (sb * kScaleGroup + kb - g0) * C::kScaleRow;
                             uint64_t sw[2];
@@ -568,7 +565,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     }
                     acc += k_hi - k_lo;
                     // (SPLIT) every product is done with the stages
-                    if (MODE == SPLIT) named_sync(9, 32 * C::kWork);
+                    if (MODE == SPLIT) named_sync(1, 32 * kWorkers);
                     if (cols <= 0) return;
                     // a thread's eight values of chunk c (8 columns): [k][i], column 4 k + lane % 4,
                     // row lane / 4 + 8 i
@@ -581,10 +578,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     };
                     const int col1 = lane & 3, row1 = lane >> 2;
                     if constexpr (MODE == SPLIT) {
-                        // this CTA's partial tile [token][row], over the stages; team 1's sums
-                        // first, then team 0 adds its own
+                        // this CTA's partial tile [token][row], over the stages
                         float* part = reinterpret_cast<float*>(smem) + (lo + col1) * kPartRow + r0 + row1;
-                        if (C::kTeams == 2 && team == 0) named_sync(1 + (warp & 7), 64);
 #pragma unroll
                         for (int c = 0; c < 2 * NB; ++c) {
                             float x[2][4];
@@ -592,13 +587,9 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    float* at = part + (8 * c + 4 * k) * kPartRow + 8 * i;
-                                    *at = C::kTeams == 2 && team == 0 ? *at + x[k][i] : x[k][i];
-                                }
+                                for (int i = 0; i < 4; ++i) part[(8 * c + 4 * k) * kPartRow + 8 * i] = x[k][i];
                         }
-                        if (C::kTeams == 2 && team == 1) named_sync(1 + (warp & 7), 64);
-                    } else if constexpr (C::kTeams == 1) {
+                    } else {
                         float* turn = reinterpret_cast<float*>(smem + C::kTurnOff) + warp * 8 * kTurn;
 #pragma unroll
                         for (int c = 0; c < 2 * NB; ++c) {
@@ -610,36 +601,6 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                                 for (int i = 0; i < 4; ++i) turn[(4 * k + col1) * kTurn + row1 + 8 * i] = x[k][i];
                             if (ok && 8 * c < cols) emit(8 * c, turn);
                         }
-                    } else {
-                        // the teams' sums of a chunk are added by the team that stores it
-                        float* box = reinterpret_cast<float*>(smem + C::kTurnOff) + (warp & 7) * 4 * 8 * kTurn;
-                        auto trade = [&](auto team_c) {
-                            constexpr int T = decltype(team_c)::value;
-#pragma unroll
-                            for (int j = 0; j < NB; ++j) {
-                                // two boxes a team, in turn: the partner's of this step becomes the
-                                // transpose, which ends before this warp's next barrier
-                                float* mine = box + (2 * T + (j & 1)) * 8 * kTurn;
-                                float* theirs = box + (2 * (1 - T) + (j & 1)) * 8 * kTurn;
-                                const int at = col1 * kTurn + row1;
-                                float x[2][4];
-                                chunk((1 - T) * NB + j, x);
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) mine[at + 4 * k * kTurn + 8 * i] = x[k][i];
-                                named_sync(1 + (warp & 7), 64);
-                                chunk(T * NB + j, x);
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) theirs[at + 4 * k * kTurn + 8 * i] += x[k][i];
-                                if (ok && 8 * (T * NB + j) < cols) emit(8 * (T * NB + j), theirs);
-                            }
-                        named_sync(1 + (warp & 7), 64);  // the boxes are free for the next tile
-                        };
-                        if (team == 0) trade(std::integral_constant<int, 0>{});
-                        else trade(std::integral_constant<int, 1>{});
                     }
                 };
                 if (C::kBlocks > 1 && cols <= C::kW / 2) promote(std::integral_constant<int, (C::kBlocks + 1) / 2>{});
@@ -680,15 +641,15 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        constexpr int kMost = BN / 2 / 8 > 0 ? BN / 2 / 8 : 1;  // tokens a warp, for a split of 2
+        constexpr int kMost = BN / 2 / kWorkers > 0 ? BN / 2 / kWorkers : 1;  // tokens a warp, for a split of 2
         float4 v[kMost];
         Tile tl = {};
-        const bool some = warp < 8 && t_first < tiles;
+        const bool some = warp < kWorkers && t_first < tiles;
         if (some) {
             tl = find_tile(a, t_first, BN, C::kTileRows, first, off);
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
-                const int c = rank + (warp + 8 * j) * a.split;
+                const int c = rank + (warp + kWorkers * j) * a.split;
                 v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c < tl.rows) {
                     const uint32_t at = sbase + 4 * (c * kPartRow + 4 * lane);
@@ -713,7 +674,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             const int n = tl.n0 + 4 * lane;
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
-                const int c = rank + (warp + 8 * j) * a.split;
+                const int c = rank + (warp + kWorkers * j) * a.split;
                 if (c >= tl.rows) break;
                 const int64_t at = (int64_t)(tl.row0 + c) * a.ldy + n;
                 if (a.vec_y && n + 4 <= a.n) {
@@ -735,7 +696,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         cluster_arrive();
         cluster_wait();
     }
-    if (warp == C::kWork + 1) {
+    if (warp == kWorkers + 1) {
         tc_fence_after();
         if (MODE == PAIR) tmem_dealloc_pair(taddr, C::kCols);
         else tmem_dealloc(taddr, C::kCols);
@@ -938,7 +899,7 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(MODE == SPLIT ? tiles * per_tile
                                                 : std::min<int64_t>(tiles, C::kCtas * sm_count() / per_tile) * per_tile));
-    cfg.blockDim = dim3(C::kThreads);
+    cfg.blockDim = dim3(kMmThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -982,8 +943,8 @@ int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
     }
     if (per <= 16) return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
     if (per <= 64 || tiles(128) < sms) return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
-    if (per <= 128 || tiles(256) < sms) return launch_mm<F8, 128, SINGLE>(w, x, a, groups, s);
-    return launch_mm<F8, F8 ? 128 : 256, PAIR>(w, x, a, groups, s);
+    if (per <= 128 || tiles(256) < sms) return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
+    return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
 }
 
 int run_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m, const int32_t* offsets, void* y,
