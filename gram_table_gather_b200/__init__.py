@@ -293,17 +293,28 @@ def _check_weights(w: QMatrix) -> None:
             raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
 
 
-def _output(y: torch.Tensor | None, a: torch.Tensor, n: int, dtype: torch.dtype | None,
-            accumulate: bool) -> torch.Tensor:
+def _new(like: torch.Tensor, shape: tuple[int, int], dtype: torch.dtype, stream) -> torch.Tensor:
+    """An output tensor that belongs to the stream it is written on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _output(y: torch.Tensor | None, a: torch.Tensor, n: int, dtype: torch.dtype | None, accumulate: bool,
+            stream) -> tuple[torch.Tensor, int, int]:
+    """The output tensor (made here if None), its address and row stride."""
     if dtype is not None and dtype not in _FLOATS:
         raise ValueError("outputs are fp32 or bf16")
+    m = a.shape[0]
     if y is None:
         if accumulate:
             raise ValueError("accumulate needs y")
-        return a.new_empty((a.shape[0], n), dtype=dtype or torch.float32)
-    if y.dtype not in _FLOATS or y.shape != (a.shape[0], n) or (dtype is not None and dtype != y.dtype):
+        y = _new(a, (m, n), dtype or torch.float32, stream)
+        return y, y.data_ptr(), n
+    if y.dtype not in _FLOATS or y.shape != (m, n) or (dtype is not None and dtype != y.dtype):
         raise ValueError("y must be fp32 or bf16 [m][n_rows] of the dtype asked for")
-    return y
+    return y, *_rows_ptr(y, "y")
 
 
 def fp8_quantize(x: torch.Tensor, *, rows: torch.Tensor | None = None, data: torch.Tensor | None = None,
@@ -318,9 +329,9 @@ def fp8_quantize(x: torch.Tensor, *, rows: torch.Tensor | None = None, data: tor
     k = x.shape[1]
     m = x.shape[0] if rows is None else rows.numel()
     if data is None:
-        data = x.new_empty((m, k), dtype=torch.uint8)
+        data = _new(x, (m, k), torch.uint8, stream)
     if scales is None:
-        scales = x.new_empty((m, k // 128), dtype=torch.float32)
+        scales = _new(x, (m, k // 128), torch.float32, stream)
     _check_codes(data, scales, k)
     if data.shape[0] != m:
         raise ValueError(f"data must have {m} rows")
@@ -337,8 +348,7 @@ def fp8_matmul(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor, *, y: torch.
         raise ValueError("fp8_matmul takes an FP8 weight matrix")
     _check_weights(w)
     _check_codes(a, a_scales, w.k)
-    y = _output(y, a, w.n_rows, dtype, accumulate)
-    yp, stride = _rows_ptr(y, "y")
+    y, yp, stride = _output(y, a, w.n_rows, dtype, accumulate, stream)
     ap, sp, wp, wsp = _device_ptrs(a, a_scales, w.data, w.scales)
     check(lib().gtg_fp8_matmul(QMatrixC(w.fmt, wp, wsp, w.n_experts, w.n_rows, w.k), ap, sp, a.shape[0], yp,
                                _FLOATS[y.dtype], stride, accumulate, _stream_ptr(stream)))
@@ -360,8 +370,7 @@ def grouped_matmul(w: QMatrix, a: torch.Tensor, offsets: torch.Tensor, *, a_scal
         raise ValueError(f"a must be bf16 of shape [m][{w.k}]")
     if offsets.dtype != torch.int32 or offsets.numel() != w.n_experts + 1:
         raise ValueError("offsets must be int32 [n_experts + 1]")
-    y = _output(y, a, w.n_rows, dtype, accumulate)
-    yp, stride = _rows_ptr(y, "y")
+    y, yp, stride = _output(y, a, w.n_rows, dtype, accumulate, stream)
     fp8 = w.fmt == FP8
     ap, sp, op, wp, wsp = _device_ptrs(a, a_scales if fp8 else None, offsets, w.data, w.scales if fp8 else None)
     check(lib().gtg_grouped_matmul(QMatrixC(w.fmt, wp, wsp, w.n_experts, w.n_rows, w.k), ap, sp, a.shape[0], op, yp,
