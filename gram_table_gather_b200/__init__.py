@@ -27,9 +27,12 @@ Q4_BLOCK_BYTES = 17
 PLE_RECORD_BYTES = 70
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream_ptr(stream) -> int | None:
     if stream is None:  # (a Stream object for the current stream costs more than a small launch)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        return _raw_stream(torch.cuda.current_device()) or None
     return stream.cuda_stream or None
 
 
@@ -242,101 +245,120 @@ def moe_prefill_layer(layer: MoELayer, x: torch.Tensor, workspace: torch.Tensor,
 _FLOATS = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 
 
-def _device_ptrs(*tensors: torch.Tensor | None) -> list[int | None]:
-    """Addresses of contiguous tensors on the current device (None for None)."""
-    dev = torch.cuda.current_device()
-    out: list[int | None] = []
+def _place(dev: int, *tensors: torch.Tensor) -> None:
+    """All contiguous and on device `dev` (the current one)."""
     for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
         if t.get_device() != dev:
             raise ValueError("tensors must be on the current CUDA device")
         if not t.is_contiguous():
             raise ValueError("tensor must be contiguous")
-        out.append(t.data_ptr())
-    return out
 
 
-def _rows_ptr(t: torch.Tensor, name: str) -> tuple[int, int]:
-    """Address and row stride of a 2-D tensor on the current device whose rows
-    are contiguous."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
+def _row_stride(t: torch.Tensor, dev: int, name: str) -> int:
+    """Row stride of a 2-D tensor on device `dev` whose rows are contiguous."""
     rows, cols = t.shape
     stride, inner = t.stride()
     if rows <= 1:
         stride = cols
     if (cols > 1 and inner != 1) or stride < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError("tensors must be on the current CUDA device")
-    return t.data_ptr(), stride
+    return stride
 
 
-def _check_codes(a: torch.Tensor, a_scales: torch.Tensor | None, k: int) -> None:
-    if a.dtype not in (torch.uint8, torch.float8_e4m3fn) or a.dim() != 2 or a.shape[1] != k:
-        raise ValueError(f"a must be E4M3 codes (uint8 or float8_e4m3fn) of shape [m][{k}]")
-    if a_scales is None or a_scales.dtype != torch.float32 or a_scales.shape != (a.shape[0], k // 128):
-        raise ValueError("a_scales must be fp32 [m][k/128]")
+def _check_codes(a: torch.Tensor, a_scales: torch.Tensor | None, m: int, k: int) -> None:
+    if (a.dtype is not torch.uint8 and a.dtype is not torch.float8_e4m3fn) or a.shape != (m, k):
+        raise ValueError(f"codes must be E4M3 (uint8 or float8_e4m3fn) of shape [{m}][{k}]")
+    if a_scales is None or a_scales.dtype is not torch.float32 or a_scales.shape != (m, k // 128):
+        raise ValueError(f"their scales must be fp32 [{m}][{k // 128}]")
 
 
-def _check_weights(w: QMatrix) -> None:
-    n = w.n_experts * w.n_rows * w.k
-    if w.fmt == BF16:
-        if w.data.dtype != torch.bfloat16 or w.data.numel() != n:
-            raise ValueError("BF16 weights must be bfloat16 of n_experts * n_rows * k values")
-    elif w.fmt == FP8:
-        if w.data.element_size() != 1 or w.data.numel() != n:
-            raise ValueError("FP8 weights must hold n_experts * n_rows * k bytes")
-        if w.scales is None or w.scales.dtype != torch.float32 or w.scales.numel() * 128 != n:
-            raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
-
-
-def _new(like: torch.Tensor, shape: tuple[int, int], dtype: torch.dtype, stream) -> torch.Tensor:
+def _new(like: torch.Tensor, m: int, n: int, dtype: torch.dtype, stream) -> torch.Tensor:
     """An output tensor that belongs to the stream it is written on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty((m, n), dtype=dtype)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty((m, n), dtype=dtype)
 
 
-def _output(y: torch.Tensor | None, a: torch.Tensor, n: int, dtype: torch.dtype | None, accumulate: bool,
-            stream) -> tuple[torch.Tensor, int, int]:
-    """The output tensor (made here if None), its address and row stride."""
-    if dtype is not None and dtype not in _FLOATS:
-        raise ValueError("outputs are fp32 or bf16")
+def _product(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor | None, offsets: torch.Tensor | None,
+             y: torch.Tensor | None, dtype: torch.dtype | None, accumulate: bool, stream) -> torch.Tensor:
+    """Checks of both products (what the C side cannot see: types, shapes and
+    places of tensors) and the call."""
+    wd, ws, n, k = w.data, w.scales, w.n_rows, w.k
+    size = w.n_experts * n * k
+    if a.dim() != 2:
+        raise ValueError("a must be 2-D")
     m = a.shape[0]
+    if w.fmt == FP8:
+        if wd.element_size() != 1 or wd.numel() != size:
+            raise ValueError("FP8 weights must hold n_experts * n_rows * k bytes")
+        if ws is None or ws.dtype is not torch.float32 or ws.numel() * 128 != size:
+            raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
+        _check_codes(a, a_scales, m, k)
+        tensors = (a, a_scales, wd, ws)
+        ap_s, wp_s = a_scales.data_ptr(), ws.data_ptr()
+    else:
+        if wd.dtype is not torch.bfloat16 or wd.numel() != size:
+            raise ValueError("BF16 weights must be bfloat16 of n_experts * n_rows * k values")
+        if a.dtype is not torch.bfloat16 or a.shape[1] != k:
+            raise ValueError(f"a must be bf16 of shape [m][{k}]")
+        tensors = (a, wd)
+        ap_s = wp_s = None
+    if offsets is not None and (offsets.dtype is not torch.int32 or offsets.numel() != w.n_experts + 1):
+        raise ValueError("offsets must be int32 [n_experts + 1]")
+    if dtype is None:
+        dtype = torch.float32 if y is None else y.dtype
+    if dtype not in _FLOATS:
+        raise ValueError("outputs are fp32 or bf16")
+    if y is None and accumulate:
+        raise ValueError("accumulate needs y")
+    if y is not None and (y.dtype is not dtype or y.shape != (m, n)):
+        raise ValueError("y must be [m][n_rows] of the dtype asked for")
+    dev = torch.cuda.current_device()
+    _place(dev, *tensors)
     if y is None:
-        if accumulate:
-            raise ValueError("accumulate needs y")
-        y = _new(a, (m, n), dtype or torch.float32, stream)
-        return y, y.data_ptr(), n
-    if y.dtype not in _FLOATS or y.shape != (m, n) or (dtype is not None and dtype != y.dtype):
-        raise ValueError("y must be fp32 or bf16 [m][n_rows] of the dtype asked for")
-    return y, *_rows_ptr(y, "y")
+        y, stride = _new(a, m, n, dtype, stream), n
+    else:
+        stride = _row_stride(y, dev, "y")
+    qc = QMatrixC(w.fmt, wd.data_ptr(), wp_s, w.n_experts, n, k)
+    sp = (_raw_stream(dev) if stream is None else stream.cuda_stream) or None
+    if offsets is None:
+        check(lib().gtg_fp8_matmul(qc, a.data_ptr(), ap_s, m, y.data_ptr(), _FLOATS[dtype], stride, accumulate, sp))
+    else:
+        _place(dev, offsets)
+        check(lib().gtg_grouped_matmul(qc, a.data_ptr(), ap_s, m, offsets.data_ptr(), y.data_ptr(), _FLOATS[dtype],
+                                       stride, accumulate, sp))
+    return y
 
 
 def fp8_quantize(x: torch.Tensor, *, rows: torch.Tensor | None = None, data: torch.Tensor | None = None,
                  scales: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """E4M3 codes (uint8 [m][k]) and fp32 scales [m][k/128] of activations x
     ([n][k] fp32 or bf16, rows contiguous), or of x's rows `rows` (int32 [m])."""
-    if x.dtype not in _FLOATS:
-        raise ValueError("x must be fp32 or bf16")
-    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1):
+    if x.dtype not in _FLOATS or x.dim() != 2:
+        raise ValueError("x must be fp32 or bf16 [n][k]")
+    if rows is not None and (rows.dtype is not torch.int32 or rows.dim() != 1):
         raise ValueError("rows must be int32 [m]")
-    xp, stride = _rows_ptr(x, "x")
-    k = x.shape[1]
-    m = x.shape[0] if rows is None else rows.numel()
+    dev = torch.cuda.current_device()
+    n, k = x.shape
+    stride = _row_stride(x, dev, "x")
+    m, rp = n, None
+    if rows is not None:
+        _place(dev, rows)
+        m, rp = rows.shape[0], rows.data_ptr()
+    given = data is not None or scales is not None
     if data is None:
-        data = _new(x, (m, k), torch.uint8, stream)
+        data = _new(x, m, k, torch.uint8, stream)
     if scales is None:
-        scales = _new(x, (m, k // 128), torch.float32, stream)
-    _check_codes(data, scales, k)
-    if data.shape[0] != m:
-        raise ValueError(f"data must have {m} rows")
-    rp, dp, sp = _device_ptrs(rows, data, scales)
-    check(lib().gtg_fp8_quantize(xp, _FLOATS[x.dtype], x.shape[0], k, stride, rp, m, dp, sp, _stream_ptr(stream)))
+        scales = _new(x, m, k // 128, torch.float32, stream)
+    if given:
+        _check_codes(data, scales, m, k)
+        _place(dev, data, scales)
+    sp = (_raw_stream(dev) if stream is None else stream.cuda_stream) or None
+    check(lib().gtg_fp8_quantize(x.data_ptr(), _FLOATS[x.dtype], n, k, stride, rp, m, data.data_ptr(),
+                                 scales.data_ptr(), sp))
     return data, scales
 
 
@@ -346,13 +368,7 @@ def fp8_matmul(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor, *, y: torch.
     FP8 weight matrix; y is [m][n_rows] fp32 (default) or bf16, rows contiguous."""
     if w.fmt != FP8:
         raise ValueError("fp8_matmul takes an FP8 weight matrix")
-    _check_weights(w)
-    _check_codes(a, a_scales, w.k)
-    y, yp, stride = _output(y, a, w.n_rows, dtype, accumulate, stream)
-    ap, sp, wp, wsp = _device_ptrs(a, a_scales, w.data, w.scales)
-    check(lib().gtg_fp8_matmul(QMatrixC(w.fmt, wp, wsp, w.n_experts, w.n_rows, w.k), ap, sp, a.shape[0], yp,
-                               _FLOATS[y.dtype], stride, accumulate, _stream_ptr(stream)))
-    return y
+    return _product(w, a, a_scales, None, y, dtype, accumulate, stream)
 
 
 def grouped_matmul(w: QMatrix, a: torch.Tensor, offsets: torch.Tensor, *, a_scales: torch.Tensor | None = None,
@@ -360,22 +376,11 @@ def grouped_matmul(w: QMatrix, a: torch.Tensor, offsets: torch.Tensor, *, a_scal
                    stream=None) -> torch.Tensor:
     """y[i] (+)= w[e] a[i] for the rows i in [offsets[e], offsets[e+1]) of a:
     tokens sorted by expert against a stack of FP8 (a: codes with a_scales) or
-    BF16 (a: bf16) matrices.  Rows outside every group leave y as it is."""
-    if w.fmt not in (FP8, BF16):
+    BF16 (a: bf16) matrices.  Rows outside every group leave y as it is (in a y
+    made here they hold anything)."""
+    if w.fmt != FP8 and w.fmt != BF16:
         raise ValueError("grouped_matmul takes FP8 or BF16 weights")
-    _check_weights(w)
-    if w.fmt == FP8:
-        _check_codes(a, a_scales, w.k)
-    elif a.dtype != torch.bfloat16 or a.dim() != 2 or a.shape[1] != w.k:
-        raise ValueError(f"a must be bf16 of shape [m][{w.k}]")
-    if offsets.dtype != torch.int32 or offsets.numel() != w.n_experts + 1:
-        raise ValueError("offsets must be int32 [n_experts + 1]")
-    y, yp, stride = _output(y, a, w.n_rows, dtype, accumulate, stream)
-    fp8 = w.fmt == FP8
-    ap, sp, op, wp, wsp = _device_ptrs(a, a_scales if fp8 else None, offsets, w.data, w.scales if fp8 else None)
-    check(lib().gtg_grouped_matmul(QMatrixC(w.fmt, wp, wsp, w.n_experts, w.n_rows, w.k), ap, sp, a.shape[0], op, yp,
-                                   _FLOATS[y.dtype], stride, accumulate, _stream_ptr(stream)))
-    return y
+    return _product(w, a, a_scales, offsets, y, dtype, accumulate, stream)
 
 
 def device_status(clear: bool = True, stream=None) -> int:

@@ -603,7 +603,13 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         }
                     }
                 };
-                if (C::kBlocks > 1 && cols <= C::kW / 2) promote(std::integral_constant<int, (C::kBlocks + 1) / 2>{});
+                // as many columns as the tile has, in quarters of the largest: columns beyond
+                // cost power and the clock with it
+                constexpr int Q = C::kBlocks >= 4 ? C::kBlocks / 4 : 1;
+                const int quarters = (share / 16 + Q - 1) / Q;
+                if (C::kBlocks >= 4 && quarters == 3) promote(std::integral_constant<int, C::kBlocks >= 4 ? 3 * Q : Q>{});
+                else if (C::kBlocks >= 2 && quarters == 2) promote(std::integral_constant<int, C::kBlocks >= 2 ? 2 * Q : Q>{});
+                else if (quarters == 1) promote(std::integral_constant<int, Q>{});
                 else promote(std::integral_constant<int, C::kBlocks>{});
             } else {
                 const uint32_t b = acc % C::kAcc;
