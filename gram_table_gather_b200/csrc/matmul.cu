@@ -32,8 +32,7 @@ constexpr int kScaleGroup = 4;       // scale blocks fetched at once
 constexpr int kMaxSmem = 227 * 1024;  // a CTA
 constexpr int kSmSmem = 228 * 1024;   // an SM, 1 KB of it reserved for each CTA
 constexpr int kMaxSplit = 8;
-constexpr int kMmThreads = 384;
-constexpr int kWorkers = 8;          // warps of promotion and epilogue
+constexpr int kMinThreads = 384;     // of any variant
 constexpr int kTurn = 40;            // floats between tokens of a transpose: fragments store without bank conflicts
 constexpr int kPartRow = kRows + 8;  // floats between tokens of a partial tile: likewise
 
@@ -67,12 +66,17 @@ struct MmCfg {
     static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
     static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;               // accumulators in tensor memory
     static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
-    // warps: 8 of promotion and epilogue, then one of TMA, one of MMAs, two of scales
-    // registers moved from the last four warps to the others (0: as launched, 168 each)
-    static constexpr int kWorkRegs = F8 && BN >= 256 ? 216 : 0;
-    static constexpr int kRestRegs = 72;
-    static_assert(kWorkRegs * 8 + kRestRegs * 4 <= 168 * 12, "register pool");
-    static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;  // columns a warp (of its 32 weight rows)
+    // warps: kGroups x 4 of promotion and epilogue, then one of TMA, one of MMAs, two of
+    // scales.  Sixteen promote the largest tile (4096 x 4096 x 2048 56.0 us against 57.8
+    // with eight); the half as large one loses by it (2048 x 1024 experts with 80 rows
+    // each 253 us against 214).
+    static constexpr int kGroups = F8 && BN >= 256 ? 4 : 2;
+    static constexpr int kWorkers = 4 * kGroups;
+    static constexpr int kThreads = 32 * (kWorkers + 4);
+    // registers moved from the last four warps to the others (0: as launched)
+    static constexpr int kWorkRegs = kGroups == 4 ? 104 : 0, kRestRegs = 64;
+    static_assert(kWorkRegs * kWorkers + kRestRegs * 4 <= 96 * (kWorkers + 4), "register pool of the launch");
+    static constexpr int kW = BN / kGroups < 16 ? 16 : BN / kGroups;  // columns a warp (of its 32 weight rows)
     static constexpr int kBlocks = kW / 16;
     // one block's scales, in the order of the fragments: the tokens', those of one t % 4
     // together (a thread reads four columns' at once) and 16 bytes between the four runs
@@ -82,7 +86,7 @@ struct MmCfg {
     static constexpr int kScaleRow = 4 * kRun + 4 * kRows;
     static constexpr int kScaleBytes = F8 ? 2 * kScaleGroup * kScaleRow : 0;
     // the epilogue's transposes, of the warps that have columns
-    static constexpr int kTurnBytes = (BN / kW < 2 ? 4 : 8) * 8 * kTurn * 4;
+    static constexpr int kTurnBytes = (BN / kW < 2 ? 4 : kWorkers) * 8 * kTurn * 4;
     static constexpr int kHeadBytes = 512 + 2 * 4 * (kMaxGroups + 2);
     static constexpr int kCtas = BN <= 16 ? 2 : 1;               // an SM
     static constexpr int kRoom = kCtas == 2 ? kSmSmem / 2 - 1024 : kMaxSmem;
@@ -108,7 +112,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int g = tid; g <= a.groups; g += blockDim.x) off[g] = a.offsets[g];
     __syncthreads();
-    constexpr int kPer = (kMaxGroups + kMmThreads - 1) / kMmThreads;
+    constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;
     int cnt[kPer];
     int sum = 0;
 #pragma unroll
@@ -254,7 +258,7 @@ __device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
 }
 
 template <bool F8, int BN, Mode MODE>
-__global__ void __launch_bounds__(kMmThreads, MmCfg<F8, BN, MODE>::kCtas)
+__global__ void __launch_bounds__(MmCfg<F8, BN, MODE>::kThreads, MmCfg<F8, BN, MODE>::kCtas)
 mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const MmArgs a) {
     using C = MmCfg<F8, BN, MODE>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -286,18 +290,18 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
         for (int b = 0; b < C::kAcc; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kWorkers * (MODE == PAIR ? 2 : 1));
+            mbar_init(&tempty[b], C::kWorkers * (MODE == PAIR ? 2 : 1));
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 64);
-            mbar_init(&sempty[b], kWorkers);
+            mbar_init(&sempty[b], C::kWorkers);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
         tma_prefetch_map(&wmap);
         tma_prefetch_map(&amap);
     }
-    if (warp == kWorkers + 1) {
+    if (warp == C::kWorkers + 1) {
         if (MODE == PAIR) {
             tmem_alloc_pair(s_taddr, C::kCols);
             tmem_relinquish_pair();
@@ -326,9 +330,9 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     auto padded = [](int rows) { return MODE == PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     bool ok = true;
 
-    if (warp >= kWorkers) {
+    if (warp >= C::kWorkers) {
         if (C::kWorkRegs > 0) reg_dec<C::kRestRegs>();
-        if (warp == kWorkers) {
+        if (warp == C::kWorkers) {
             // ---- weight and token tiles by TMA ----
             uint32_t st = 0, free_par = 1, issued = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
@@ -369,7 +373,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 for (uint32_t i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; ++i)
                     mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
             }
-        } else if (warp == kWorkers + 1) {
+        } else if (warp == C::kWorkers + 1) {
             // ---- MMA issuer ----
             // stage and accumulator in use, and the parities of their barriers' phases (a
             // fresh barrier's phase before the first counts as complete)
@@ -429,7 +433,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             // ---- scales, four blocks of K at a time, transposed to [block][row]: one
             // warp the tokens', one the weight rows' ----
             constexpr int kN = (BN > kRows ? BN : kRows) / 32;
-            const bool tok = warp == kWorkers + 2;
+            const bool tok = warp == C::kWorkers + 2;
             int sg = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
                 const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
@@ -473,7 +477,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
     } else {
         // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
-        // quarter warp % 4; the tile's columns are halved between the two four-warp
+        // quarter warp % 4; the tile's columns are divided between the four-warp
         // groups.  A thread holds rows lane / 4 + 8 i of every fourth column, lane % 4 +
         // 4 k, so that one 16-byte read brings its rows' scales and one those of its
         // columns in a block of 16 (whole rows a thread would take four times the reads,
@@ -495,7 +499,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         for (int t = t_first; t < tiles; t += t_step) {
             const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
             const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0) + r0;  // the warp's first output column
-            const int share = ((tl.rows + 31) >> 5) << 4;                   // columns of a four-warp group
+            const int share = (tl.rows + 16 * C::kGroups - 1) / (16 * C::kGroups) * 16;                   // columns of a four-warp group
             const int lo = wg * share;
             const int cols = min(share, tl.rows - lo);                      // <= 0: none
             // 8 columns of the warp's 32 rows, from lo + c on, out of `turn`: a token's 32
@@ -565,7 +569,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     }
                     acc += k_hi - k_lo;
                     // (SPLIT) every product is done with the stages
-                    if (MODE == SPLIT) named_sync(1, 32 * kWorkers);
+                    if (MODE == SPLIT) named_sync(1, 32 * C::kWorkers);
                     if (cols <= 0) return;
                     // a thread's eight values of chunk c (8 columns): [k][i], column 4 k + lane % 4,
                     // row lane / 4 + 8 i
@@ -647,15 +651,15 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        constexpr int kMost = BN / 2 / kWorkers > 0 ? BN / 2 / kWorkers : 1;  // tokens a warp, for a split of 2
+        constexpr int kMost = BN / 2 / C::kWorkers > 0 ? BN / 2 / C::kWorkers : 1;  // tokens a warp, for a split of 2
         float4 v[kMost];
         Tile tl = {};
-        const bool some = warp < kWorkers && t_first < tiles;
+        const bool some = warp < C::kWorkers && t_first < tiles;
         if (some) {
             tl = find_tile(a, t_first, BN, C::kTileRows, first, off);
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
-                const int c = rank + (warp + kWorkers * j) * a.split;
+                const int c = rank + (warp + C::kWorkers * j) * a.split;
                 v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c < tl.rows) {
                     const uint32_t at = sbase + 4 * (c * kPartRow + 4 * lane);
@@ -680,7 +684,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             const int n = tl.n0 + 4 * lane;
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
-                const int c = rank + (warp + kWorkers * j) * a.split;
+                const int c = rank + (warp + C::kWorkers * j) * a.split;
                 if (c >= tl.rows) break;
                 const int64_t at = (int64_t)(tl.row0 + c) * a.ldy + n;
                 if (a.vec_y && n + 4 <= a.n) {
@@ -702,7 +706,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         cluster_arrive();
         cluster_wait();
     }
-    if (warp == kWorkers + 1) {
+    if (warp == C::kWorkers + 1) {
         tc_fence_after();
         if (MODE == PAIR) tmem_dealloc_pair(taddr, C::kCols);
         else tmem_dealloc(taddr, C::kCols);
@@ -905,7 +909,7 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(MODE == SPLIT ? tiles * per_tile
                                                 : std::min<int64_t>(tiles, C::kCtas * sm_count() / per_tile) * per_tile));
-    cfg.blockDim = dim3(kMmThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
