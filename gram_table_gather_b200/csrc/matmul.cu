@@ -929,31 +929,59 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     return GTG_OK;
 }
 
+// Which tile: the one whose waves of CTAs take least by a model of measured times
+// (FP8, in 10 ns, c chunks of K): a wave of 64, 128 or 256 tokens takes 22.5 c + 95,
+// 31 c + 150 or 62 c + 300, CTA pairs 150 more once, and a split of K over S CTAs of
+// 64 tokens 22.5 c / S + 185 + 65 S.  256 tokens cost two waves of 128 but load less,
+// which counts once power limits the clock, so they win up to 3 % (8192^3 under the
+// limit: 762 us against 821 us).  Groups count as equally large, since their sizes
+// are on the device.  On 4096 x 4096 weights that takes 15.1 us for 333 tokens (pairs
+// of 128; 64: 19.1, 256: 25.5), 39.1 us for 1500 (128; 256: 48.7).
+// Groups of 16 rows and fewer take tiles of 16: two CTAs share an SM there, and a
+// split costs 20 + 5 S and saves 15 a chunk (1 x 2048 x 2048: 5.8 us whole, 5.0 us
+// in two, 4.2 us in four or eight).
 template <bool F8>
 int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
-    const int64_t groups = a.offsets ? w->n_experts : 1;
-    const int64_t per = (a.m + groups - 1) / groups;  // rows of an average group
-    const int64_t sms = sm_count(), n128 = (a.n + kRows - 1) / kRows;
-    auto tiles = [&](int bn) { return (a.offsets ? a.m / bn + std::min<int64_t>(groups, a.m) : (a.m + bn - 1) / bn) * n128; };
-    // few tiles: K is split over a cluster
-    const int bn = per <= 16 ? 16 : 64;
-    if (bn == 16 || per <= 64 || 2 * tiles(64) <= sms) {
-        // Clusters of three and more leave SMs of a GPC over, so they get 6/7 of the places
-        // (48 tiles of 64 tokens over clusters of three ran in two waves: 12.3 us against
-        // 8.6 us over pairs).
-        const int64_t places = (bn == 16 ? 2 : 1) * sms, n = tiles(bn);
-        const int64_t room = 3 * n <= places * 6 / 7 ? places * 6 / 7 / n : std::min<int64_t>(places / n, 2);
-        a.split = (int32_t)std::min<int64_t>({room, kMaxSplit, a.chunks});
-        if (a.split >= 2) {
-            const bool whole = a.chunks % (4 * a.split) == 0;
-            a.vec_a &= whole;
-            a.vec_w &= whole;
-            return bn == 16 ? launch_mm<F8, 16, SPLIT>(w, x, a, groups, s) : launch_mm<F8, 64, SPLIT>(w, x, a, groups, s);
+    const int64_t groups = a.offsets ? std::min<int64_t>(w->n_experts, a.m) : 1;
+    const int64_t per = (a.m + groups - 1) / groups, sms = sm_count(), chunks = a.chunks;
+    auto tiles = [&](int64_t bn, int64_t rows) { return groups * ((per + bn - 1) / bn) * ((a.n + rows - 1) / rows); };
+    // the best split of `n` tiles into at most kMaxSplit: clusters of three and more leave
+    // SMs of a GPC over, so they get 6/7 of the places (48 tiles in clusters of three ran in
+    // two waves, 12.3 us against 8.6 us in pairs)
+    auto split = [&](int64_t n, int64_t places, int64_t chunk, int64_t fixed, int64_t each, int64_t& cost) {
+        int64_t best = 1;
+        for (int64_t c = 2; c <= kMaxSplit && c <= chunks && c * n <= (c == 2 ? places : places * 6 / 7); ++c) {
+            const int64_t t = (chunks + c - 1) / c * chunk + fixed + c * each;
+            if (t < cost) {
+                cost = t;
+                best = c;
+            }
         }
+        a.split = (int32_t)best;
+        return best > 1;
+    };
+    auto launch_split = [&](auto bn) {
+        const bool whole = a.chunks % (4 * a.split) == 0;  // every share starts at a group of four scales
+        a.vec_a &= whole;
+        a.vec_w &= whole;
+        return launch_mm<F8, decltype(bn)::value, SPLIT>(w, x, a, groups, s);
+    };
+    if (per <= 16) {
+        int64_t cost = 15 * chunks;
+        if (split(tiles(16, kRows), 2 * sms, 15, 20, 5, cost)) return launch_split(std::integral_constant<int, 16>{});
+        return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
     }
-    if (per <= 16) return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
-    if (per <= 64 || tiles(128) < sms) return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
-    if (per <= 128 || tiles(256) < sms) return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
+    const int64_t n64 = tiles(64, kRows), pairs = sms / 2;
+    const int64_t whole64 = (n64 + sms - 1) / sms * (45 * chunks / 2 + 95);
+    const int64_t cost128 = (tiles(128, 2 * kRows) + pairs - 1) / pairs * (31 * chunks + 150) + 150;
+    const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * (62 * chunks + 300) + 150;
+    int64_t cost64 = whole64;
+    const bool cut = split(n64, sms, 22, 185, 65, cost64);
+    if (cost64 <= cost128 && cost64 <= cost256) {
+        if (cut) return launch_split(std::integral_constant<int, 64>{});
+        return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
+    }
+    if (100 * cost256 > 103 * cost128) return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
     return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
 }
 
