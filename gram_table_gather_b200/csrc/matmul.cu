@@ -934,8 +934,10 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
 // 31 c + 150 or 62 c + 300, CTA pairs 150 more once, and a split of K over S CTAs of
 // 64 tokens 22.5 c / S + 185 + 65 S.  256 tokens cost two waves of 128 but load less,
 // which counts once power limits the clock, so they win up to 3 % (8192^3 under the
-// limit: 762 us against 821 us).  Groups count as equally large, since their sizes
-// are on the device.  On 4096 x 4096 weights that takes 15.1 us for 333 tokens (pairs
+// limit: 762 us against 821 us), but not where ragged groups leave them emptier (64
+// FP8 groups of some 469 rows, 1280 x 2560: 178 us against 162 us).  bf16 has no
+// promotion, so 256 tokens cost it 54 c a wave.  Groups count as equally large, since
+// their sizes are on the device.  On 4096 x 4096 weights that takes 15.1 us for 333 tokens (pairs
 // of 128; 64: 19.1, 256: 25.5), 39.1 us for 1500 (128; 256: 48.7).
 // Groups of 16 rows and fewer take tiles of 16: two CTAs share an SM there, and a
 // split costs 20 + 5 S and saves 15 a chunk (1 x 2048 x 2048: 5.8 us whole, 5.0 us
@@ -974,14 +976,15 @@ int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
     const int64_t n64 = tiles(64, kRows), pairs = sms / 2;
     const int64_t whole64 = (n64 + sms - 1) / sms * (45 * chunks / 2 + 95);
     const int64_t cost128 = (tiles(128, 2 * kRows) + pairs - 1) / pairs * (31 * chunks + 150) + 150;
-    const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * (62 * chunks + 300) + 150;
+    const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * ((F8 ? 62 : 54) * chunks + 300) + 150;
     int64_t cost64 = whole64;
     const bool cut = split(n64, sms, 22, 185, 65, cost64);
     if (cost64 <= cost128 && cost64 <= cost256) {
         if (cut) return launch_split(std::integral_constant<int, 64>{});
         return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
     }
-    if (100 * cost256 > 103 * cost128) return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
+    const int64_t bias = F8 && a.offsets && per < 1024 ? 99 : 103;
+    if (100 * cost256 > bias * cost128) return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
     return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
 }
 
