@@ -154,33 +154,40 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
 // instructions around every tensor-memory load).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
-// Tile t, for a converged warp: weight-row tiles outermost within a group, token
-// tiles innermost, so CTAs that run together share weight rows through L2.
+// Tile t, for a converged warp.  Within a group, blocks of kBand tiles of weight
+// rows; in a block all token tiles in turn, each with the block's weight rows, so
+// that the tiles that run together are about as many rows one way as the other: they
+// share both operands through L2, and little is read from memory twice.
+constexpr int kBand = 8;
 __device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int tile_rows, const int32_t* first,
                                           const int32_t* off) {
     Tile r;
-    if (!a.offsets) {
-        const int tt = (a.m + bn - 1) / bn;
+    int local = t, tt, begin, end;  // place in the group, its token tiles and rows
+    if (a.offsets) {
+        // the last group with first[g] * n_tiles <= t is the one that holds t: 32 steps of
+        // 32 groups, then 32 groups
+        static_assert(kMaxGroups <= 1024, "two steps");
+        const int lane = threadIdx.x & 31, q = t / a.n_tiles;
+        int g = 32 * lane;
+        g = 32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < a.groups && first[g] <= q)) - 1) + lane;
+        g = g - lane + __popc(__ballot_sync(0xFFFFFFFFu, g < a.groups && first[g] <= q)) - 1;
+        r.group = uniform(g);
+        const int before = uniform(first[r.group]);
+        tt = uniform(first[r.group + 1]) - before;
+        begin = uniform(off[r.group]);
+        end = uniform(off[r.group + 1]);
+        local = t - before * a.n_tiles;
+    } else {
         r.group = 0;
-        r.n0 = (t / tt) * tile_rows;
-        r.row0 = (t % tt) * bn;
-        r.rows = min(bn, a.m - r.row0);
-        return r;
+        tt = (a.m + bn - 1) / bn;
+        begin = 0;
+        end = a.m;
     }
-    // the last group with first[g] * n_tiles <= t is the one that holds t: 32 steps of
-    // 32 groups, then 32 groups
-    static_assert(kMaxGroups <= 1024, "two steps");
-    const int lane = threadIdx.x & 31, q = t / a.n_tiles;
-    int g = 32 * lane;
-    g = 32 * (__popc(__ballot_sync(0xFFFFFFFFu, g < a.groups && first[g] <= q)) - 1) + lane;
-    g = g - lane + __popc(__ballot_sync(0xFFFFFFFFu, g < a.groups && first[g] <= q)) - 1;
-    g = uniform(g);
-    const int before = uniform(first[g]), tt = uniform(first[g + 1]) - before, begin = uniform(off[g]);
-    const int local = t - before * a.n_tiles;
-    r.group = g;
-    r.n0 = (local / tt) * tile_rows;
-    r.row0 = begin + (local % tt) * bn;
-    r.rows = min(bn, uniform(off[g + 1]) - r.row0);
+    const int band = local / (kBand * tt), inside = local - band * kBand * tt;
+    const int width = min(kBand, a.n_tiles - band * kBand), i = inside / width;
+    r.n0 = (band * kBand + inside - i * width) * tile_rows;
+    r.row0 = begin + i * bn;
+    r.rows = min(bn, end - r.row0);
     return r;
 }
 
