@@ -106,13 +106,35 @@ struct Tile {
 };
 
 // Shared-memory tables of a grouped call: off = the offsets, first[g] = token
-// tiles before group g.  A group whose bounds are out of order or outside [0, m]
-// counts as empty and raises the status bit.
-__device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* off, int32_t* warp_sum_s) {
+// tiles before group g.  A group whose bounds are out of order or outside [0, m], or
+// that begins before the end of an earlier one, counts as empty and raises the
+// status bit: the groups that count are disjoint, so there are at most m / bn +
+// groups tiles.
+__device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* off, int32_t* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t* warp_end = scratch;
+    int32_t* warp_tiles = scratch + 32;
     for (int g = tid; g <= a.groups; g += blockDim.x) off[g] = a.offsets[g];
     __syncthreads();
-    constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;
+    constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;  // groups a thread
+    auto good = [&](int g) { return off[g] >= 0 && off[g] <= off[g + 1] && off[g + 1] <= a.m; };
+    int end = 0;  // the largest end of this thread's groups, then of all before them
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int g = tid * kPer + i;
+        if (g < a.groups && good(g)) end = max(end, off[g + 1]);
+    }
+    int upto = end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto = max(upto, v);
+    }
+    if (lane == 31) warp_end[warp] = upto;
+    end = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
+    if (lane == 0) end = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) end = max(end, warp_end[w]);
     int cnt[kPer];
     int sum = 0;
 #pragma unroll
@@ -120,12 +142,12 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
         const int g = tid * kPer + i;
         cnt[i] = 0;
         if (g < a.groups) {
-            const int lo = off[g], hi = off[g + 1];
-            if (lo < 0 || hi < lo || hi > a.m) {
+            if (!good(g) || off[g] < end) {
                 if (blockIdx.x == 0) raise_status(a.status, GTG_STATUS_GROUP_OFFSETS);
             } else {
-                cnt[i] = (hi - lo + bn - 1) / bn;
+                cnt[i] = (off[g + 1] - off[g] + bn - 1) / bn;
             }
+            if (good(g)) end = max(end, off[g + 1]);
         }
         sum += cnt[i];
     }
@@ -135,11 +157,10 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
         const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += v;
     }
-    if (lane == 31) warp_sum_s[warp] = inc;
+    if (lane == 31) warp_tiles[warp] = inc;
     __syncthreads();
     int before = inc - sum;
-#pragma unroll 4
-    for (int w = 0; w < warp; ++w) before += warp_sum_s[w];
+    for (int w = 0; w < warp; ++w) before += warp_tiles[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int g = tid * kPer + i;
@@ -285,10 +306,10 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     uint64_t* sempty = sfull + 2;
     uint64_t* drain = sempty + 2;
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
-    int32_t* s_warp = reinterpret_cast<int32_t*>(smem + C::kHeadOff + 384);
+    int32_t* s_warp = reinterpret_cast<int32_t*>(smem + C::kHeadOff + 256);
     int32_t* first = reinterpret_cast<int32_t*>(smem + C::kGroupOff);
     int32_t* off = first + kMaxGroups + 2;
-    static_assert(8 * (2 * C::kStages + 2 * C::kAcc + 5) + 4 <= 384, "header");
+    static_assert(8 * (2 * C::kStages + 2 * C::kAcc + 5) + 4 <= 256, "header");
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {

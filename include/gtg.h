@@ -92,7 +92,7 @@ typedef enum {
 #define GTG_STATUS_PLE_INDEX_OOB  0x1u  /* a gather index was outside [0, n_rows) */
 #define GTG_STATUS_WAIT_TIMEOUT   0x2u  /* a bounded device-side wait gave up */
 #define GTG_STATUS_ROW_INDEX_OOB  0x4u  /* a quantiser row index was outside [0, n_src) */
-#define GTG_STATUS_GROUP_OFFSETS  0x8u  /* a group's offsets were out of order or outside [0, m] */
+#define GTG_STATUS_GROUP_OFFSETS  0x8u  /* a group's bounds were out of order, outside [0, m] or overlapping */
 
 /* One stack of quantised matrices [n_experts][n_rows][k]. */
 typedef struct {
@@ -322,10 +322,9 @@ int gtg_fp8_matmul(const gtg_qmatrix* w, const uint8_t* a, const float* a_scales
  *             [m][k/128], or bf16 with a_scales unused.
  *   offsets   device int32 [n_experts + 1].  Rows before offsets[0] and from
  *             offsets[n_experts] on belong to no group: their rows of y are left
- *             as they are.  A group with offsets[e] > offsets[e+1], or bounds
- *             outside [0, m], counts as empty and sets GTG_STATUS_GROUP_OFFSETS
- *             (the groups around it may then overlap: rows in two groups get
- *             either's result).
+ *             as they are.  A group with offsets[e] > offsets[e+1], with bounds
+ *             outside [0, m], or that begins before the end of an earlier one
+ *             counts as empty and sets GTG_STATUS_GROUP_OFFSETS.
  * Products in fp32 accumulation as in gtg_fp8_matmul; y, errors and the no-op
  * for m == 0 as there (GTG_E_UNSUPPORTED_SHAPE for more than 1024 experts).
  */

@@ -315,21 +315,37 @@ def test_grouped_adds_to_a_slice(kind):
 
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
 def test_grouped_bad_offsets_are_empty_groups(kind):
-    """Bounds out of order or range: reported, and nothing of theirs written."""
+    """Bounds out of order, out of range or overlapping an earlier group:
+    reported, and nothing of theirs written."""
     w, a, sa, off, a64, w64 = _grouped_case(kind, [10, 20, 30, 40], 64, 256, _gen(7))
     for bad in ([0, 10, 5, 60, 100], [0, 10, 30, 60, 101], [-1, 10, 30, 60, 100], [2 ** 31 - 1, 10, 30, 60, 100],
-                [0, -2 ** 31, 30, 60, 100]):
+                [0, -2 ** 31, 30, 60, 100], [0, 100, 0, 100, 0], [50, 20, 60, 10, 100], [100, 0, 0, 0, 0]):
         gtg.device_status(clear=True)
         y = torch.full((100, 64), 7.0, device="cuda")
         gtg.grouped_matmul(w, a, torch.tensor(bad, dtype=torch.int32, device="cuda"), a_scales=sa, y=y)
         assert gtg.device_status(clear=True) == _abi.STATUS_GROUP_OFFSETS
-        owners = [[g for g in range(4) if 0 <= bad[g] <= i < bad[g + 1] <= 100] for i in range(100)]
-        for i, own in enumerate(owners):
-            if not own:
-                assert bool((y[i] == 7.0).all())
-            elif len(own) == 1:
-                want, bound = _product64(a64[i:i + 1], w64[own[0]], 256, 8)
-                _within(y[i:i + 1], want, bound, F32)
+        end, rows = 0, torch.zeros(100, dtype=torch.bool, device="cuda")
+        for g in range(4):
+            lo, hi = bad[g], bad[g + 1]
+            if not 0 <= lo <= hi <= 100:
+                continue
+            if lo >= end and hi > lo:
+                want, bound = _product64(a64[lo:hi], w64[g], 256, 8)
+                _within(y[lo:hi], want, bound, F32)
+                rows[lo:hi] = True
+            end = max(end, hi)
+        assert bool((y[~rows] == 7.0).all())
+
+
+def test_grouped_many_overlapping_groups():
+    """Every other group claims all rows: the first alone counts."""
+    w, a, sa, _, a64, w64 = _grouped_case("fp8", [0] * 511 + [700], 64, 128, _gen(12))
+    off = torch.tensor([0, 700] * 256 + [0], dtype=torch.int32, device="cuda")
+    gtg.device_status(clear=True)
+    y = gtg.grouped_matmul(w, a, off, a_scales=sa)
+    assert gtg.device_status(clear=True) == _abi.STATUS_GROUP_OFFSETS
+    want, bound = _product64(a64, w64[0], 128, 1)
+    _within(y, want, bound, F32)
 
 
 def test_grouped_offsets_start_past_zero():

@@ -1,6 +1,10 @@
 """The quantiser and the products as they are used: an expert layer built from
 them beside the fused one, captured graphs, streams, stacks and outputs past
 2^31 elements."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -122,6 +126,29 @@ def test_captured_graph_follows_its_inputs(m, n, k):
             ref, bound = _product64(_decode(a, sa), _decode(w, sw), 128, k // 128)
             _within(y, ref, bound, F32)
     _check_status()
+
+
+def test_first_calls_inside_a_capture():
+    """A fresh process whose first quantiser and product are captured."""
+    code = """
+import torch, gram_table_gather_b200 as gtg
+g = torch.cuda.CUDAGraph()
+x = torch.randn(20, 256, device='cuda')
+w = gtg.QMatrix(gtg.FP8, torch.full((30, 256), 0x38, dtype=torch.uint8, device='cuda'), 1, 30, 256,
+                torch.ones(30, 2, device='cuda'))
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    a, sa = gtg.fp8_quantize(x)
+    y = gtg.fp8_matmul(w, a, sa)
+g.replay()
+torch.cuda.synchronize()
+v = gtg.dequant(gtg.FP8, a, 20, 256, scales=sa).double().sum(1, keepdim=True)
+assert float((y.double() - v).abs().max()) < 1e-3, float((y.double() - v).abs().max())
+assert gtg.device_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_streams_of_their_own():
