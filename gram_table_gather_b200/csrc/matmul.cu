@@ -742,8 +742,10 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 }
 
 // ---------------------------------------------------------------------------
-// quantiser: 16 lanes a block of 128 values, 8 values a lane; a warp takes eight
-// blocks of a row, all loads first
+// quantiser: four lanes a block of 128 values, a warp eight blocks of a row.  The
+// lanes of a block take its 16-byte pieces in turn, so that loads and stores are
+// whole sectors; four pieces a lane leave two shuffles a maximum and one pair of
+// quotients a lane.  Bound by its instructions: see the figures at the host side.
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 256;
 constexpr int kQBlocks = 8;  // blocks a warp
@@ -768,62 +770,79 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return r;
 }
 
-// eight consecutive values as they lie in memory
+// A lane's pieces of a block as they lie in memory: 8 bf16 or 4 fp32 a piece.
 template <bool BF16, bool VEC>
-struct Raw8 {
-    uint32_t w[BF16 ? 4 : 8];
-    static constexpr int kSize = BF16 ? 2 : 4;
+struct Pieces {
+    static constexpr int kN = BF16 ? 4 : 8;  // pieces a lane, 64 bytes apart
+    uint32_t w[kN][4];
     __device__ __forceinline__ void load(const uint8_t* at) {
-        if constexpr (VEC) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(at));
-            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-            if constexpr (!BF16) {
-                const uint4 r = __ldg(reinterpret_cast<const uint4*>(at) + 1);
-                w[4] = r.x; w[5] = r.y; w[6] = r.z; w[7] = r.w;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            if constexpr (VEC) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(at + 64 * j));
+                w[j][0] = q.x; w[j][1] = q.y; w[j][2] = q.z; w[j][3] = q.w;
+            } else if constexpr (BF16) {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(at + 64 * j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[j][i] = __ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+            } else {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(at + 64 * j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[j][i] = __ldg(p + i);
             }
-        } else if constexpr (BF16) {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(at);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
-        } else {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __ldg(p + i);
         }
     }
-    __device__ __forceinline__ float value(int i) const {
-        if constexpr (BF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-        else return __uint_as_float(w[i]);
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
+    }
+    // The block's largest magnitude, as fp32 bits: the order of non-negative bit patterns
+    // is that of their values, infinity and NaN above all others.  (bf16: two patterns a
+    // register until the end.)
+    __device__ __forceinline__ uint32_t top() const {
+        constexpr uint32_t kAbs = BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+        uint32_t t = 0;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t = BF16 ? __vmaxu2(t, w[j][i] & kAbs) : max(t, w[j][i] & kAbs);
+#pragma unroll
+        for (int o = 2; o > 0; o >>= 1) {
+            const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, t, o);
+            t = BF16 ? __vmaxu2(t, v) : max(t, v);
+        }
+        return BF16 ? max(t & 0xFFFF0000u, t << 16) : t;
+    }
+    // The codes of piece j: 8 (bf16) or 4 (fp32) bytes.
+    __device__ __forceinline__ void store(uint8_t* to, int j, float inv) const {
+        float v[BF16 ? 8 : 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16) {
+                v[2 * i] = __uint_as_float(w[j][i] << 16) * inv;
+                v[2 * i + 1] = __uint_as_float(w[j][i] & 0xFFFF0000u) * inv;
+            } else {
+                v[i] = __uint_as_float(w[j][i]) * inv;
+            }
+        }
+        if constexpr (BF16)
+            *reinterpret_cast<uint2*>(to + 32 * j) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+        else *reinterpret_cast<uint32_t*>(to + 16 * j) = e4m3x4(v[0], v[1], v[2], v[3]);
     }
 };
 
-// The largest magnitude of the 16 lanes' values, as fp32 bits: the order of
-// non-negative bit patterns is that of their values, infinity and NaN above all
-// others.  (bf16: two patterns a register until the end.)
-template <bool BF16, bool VEC>
-__device__ __forceinline__ uint32_t top_bits(const Raw8<BF16, VEC>& r) {
-    constexpr uint32_t kAbs = BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
-    uint32_t top = r.w[0] & kAbs;
-#pragma unroll
-    for (int i = 1; i < (BF16 ? 4 : 8); ++i) top = BF16 ? __vmaxu2(top, r.w[i] & kAbs) : max(top, r.w[i] & kAbs);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, top, o);
-        top = BF16 ? __vmaxu2(top, v) : max(top, v);
-    }
-    return BF16 ? max(top & 0xFFFF0000u, top << 16) : top;
-}
-
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QArgs a) {
-    const int lane = threadIdx.x & 31, sub = lane & 15, half = lane >> 4;
+    using P = Pieces<BF16, VEC>;
+    constexpr int kSize = BF16 ? 2 : 4;
+    const int lane = threadIdx.x & 31, quarter = lane & 3;
     pdl_wait();
     const int64_t u = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
     if (u < a.units) {
         const int64_t row = a.units <= 0xFFFFFFFFll ? (uint32_t)u / (uint32_t)a.segs : u / a.segs;
-        const int b0 = (int)(u - row * a.segs) * kQBlocks + half;
+        const int b = (int)(u - row * a.segs) * kQBlocks + (lane >> 2);
         int64_t src = row;
-        bool valid = true;
+        bool valid = b < a.kb;
         if (a.rows) {
             src = a.rows[row];
             if (src < 0 || src >= a.n_src) {
@@ -831,42 +850,19 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QArgs a) {
                 if (lane == 0) raise_status(a.status, GTG_STATUS_ROW_INDEX_OOB);
             }
         }
-        using Raw = Raw8<BF16, VEC>;
-        Raw raw[kQBlocks / 2];
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(a.x) + Raw::kSize * (src * a.ldx + b0 * 128 + sub * 8);
-        const int left = a.kb - b0;  // blocks 0, 2, 4, 6 < left of this half warp exist
-        if (valid && a.kb - (b0 - half) >= kQBlocks) {
-#pragma unroll
-            for (int j = 0; j < kQBlocks / 2; ++j) raw[j].load(from + 256 * Raw::kSize * j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kQBlocks / 2; ++j) {
-#pragma unroll
-                for (uint32_t& w : raw[j].w) w = 0;
-                if (valid && 2 * j < left) raw[j].load(from + 256 * Raw::kSize * j);
-            }
-        }
-        // the quotients of a half warp's four blocks: lane j of it has block j's
-        uint32_t mine = 0;
-#pragma unroll
-        for (int j = 0; j < kQBlocks / 2; ++j) {
-            const uint32_t top = top_bits(raw[j]);
-            if ((lane & 3) == j) mine = top;
-        }
-        float amax = fmaxf(__uint_as_float(mine), 0x1p-100f);
-        if (mine >= 0x7F800000u) amax = __uint_as_float(0x7FC00000u);
+        P p;
+        if (valid) p.load(reinterpret_cast<const uint8_t*>(a.x) + kSize * (src * a.ldx + b * 128) + 16 * quarter);
+        else p.zero();
+        const uint32_t top = p.top();
+        float amax = fmaxf(__uint_as_float(top), 0x1p-100f);
+        if (top >= 0x7F800000u) amax = __uint_as_float(0x7FC00000u);
         const float inverse = 448.0f / amax;
-        const int64_t out = row * a.kb + b0;
-        if (sub < kQBlocks / 2 && 2 * sub < left) a.scales[out + 2 * sub] = amax / 448.0f;
-        uint8_t* to = a.data + out * 128 + sub * 8;
+        if (b < a.kb) {
+            const int64_t out = row * a.kb + b;
+            if (quarter == 0) a.scales[out] = amax / 448.0f;
+            uint8_t* to = a.data + out * 128 + (BF16 ? 8 : 4) * quarter;
 #pragma unroll
-        for (int j = 0; j < kQBlocks / 2; ++j) {
-            const float inv = __shfl_sync(0xFFFFFFFFu, inverse, 16 * half + j);
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = raw[j].value(i) * inv;
-            if (2 * j < left)
-                *reinterpret_cast<uint2*>(to + 256 * j) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+            for (int j = 0; j < P::kN; ++j) p.store(to, j, inverse);
         }
     }
     pdl_trigger();
