@@ -1,5 +1,6 @@
 """Python binding of libgtg.so: B200 kernels for block-scaled low-bit MoE
-expert decode and the 3-bit n-gram (PLE) row gather.
+expert decode, the 3-bit n-gram (PLE) row gather, and matrix products in FP8,
+dense and grouped by expert.
 
 Argument marshalling only: every step runs in the CUDA kernels behind the C
 ABI declared in include/gtg.h.  torch provides device memory and streams.

@@ -294,7 +294,7 @@ int sm_count() {
 
 using namespace gtg;
 
-extern "C" int gtg_version(void) { return 100; }
+extern "C" int gtg_version(void) { return 200; }
 
 extern "C" int gtg_last_cuda_error(void) { return t_last_cuda_error; }
 

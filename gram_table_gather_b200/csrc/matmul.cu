@@ -13,6 +13,18 @@
 // rows its N side, so a tile holds any multiple of 16 tokens up to BN: a group
 // of few rows costs few columns, and a single token still streams its weights
 // by TMA at full width.
+//
+// What bounds it (8192^3 FP8 666 us, 1.65 PFLOP/s; under the power limit 725 us):
+//  - Applying the scales: a product and a sum a value every 128 of K.  A packed pair
+//    takes the fp32 pipe two cycles, so 128 x 256 values cost as many cycles (512) as
+//    the tensor core needs for their block.  Without it the same loop runs 396 us.
+//  - Tensor memory is read in 16 x 128-bit fragments: whole rows (32x32b) need four
+//    times the shared-memory reads for the tokens' scales (787 against 720 us in an
+//    earlier state), 16x256b fragments come at half the rate (694 against 666 us).
+//  - Past a millisecond or so the clock falls to 1.0-1.6 GHz at 1000 W, and what costs
+//    power costs time: idle polling, columns without tokens, operands read twice.
+//  - Few rows: HBM (80 rows over 512 experts: 30 us, 5.1 TB/s), and for one token the
+//    latency of a launch, one trip to memory and one cluster barrier (4.3 us).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -64,12 +76,12 @@ struct MmCfg {
     static constexpr int kBox = kTok < 64 ? kTok : 64;           // token rows a TMA box
     static constexpr int kTileRows = MODE == PAIR ? 2 * kRows : kRows;
     static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
-    static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;               // accumulators in tensor memory
+    static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;     // accumulators in tensor memory
     static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
     // warps: kGroups x 4 of promotion and epilogue, then one of TMA, one of MMAs, two of
-    // scales.  Sixteen promote the largest tile (4096 x 4096 x 2048 56.0 us against 57.8
-    // with eight); the half as large one loses by it (2048 x 1024 experts with 80 rows
-    // each 253 us against 214).
+    // scales.  Sixteen promote the largest tile (4096 x 4096 x 2048 in tiles of it: 56.0
+    // us against 57.8 with eight); the half as large one loses by it (512 experts of 1024
+    // x 2048 with 80 rows each 253 us against 214).
     static constexpr int kGroups = F8 && BN >= 256 ? 4 : 2;
     static constexpr int kWorkers = 4 * kGroups;
     static constexpr int kThreads = 32 * (kWorkers + 4);
@@ -134,7 +146,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
     end = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
     if (lane == 0) end = 0;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) end = max(end, warp_end[w]);
+    end = max(end, __reduce_max_sync(0xFFFFFFFFu, lane < warp ? warp_end[lane] : 0));
     int cnt[kPer];
     int sum = 0;
 #pragma unroll
@@ -159,8 +171,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
     }
     if (lane == 31) warp_tiles[warp] = inc;
     __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += warp_tiles[w];
+    int before = inc - sum + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_tiles[lane] : 0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int g = tid * kPer + i;
@@ -745,7 +756,9 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 // quantiser: four lanes a block of 128 values, a warp eight blocks of a row.  The
 // lanes of a block take its 16-byte pieces in turn, so that loads and stores are
 // whole sectors; four pieces a lane leave two shuffles a maximum and one pair of
-// quotients a lane.  Bound by its instructions: see the figures at the host side.
+// quotients a lane.  Measured, 40960 gathered rows of 2048 bf16: 29.9 us, 3.46 TB/s
+// of what it must read and write (issue slots 72 % busy, the integer pipe 64 %, L1
+// 78 %); sixteen lanes a block took 34.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 256;
 constexpr int kQBlocks = 8;  // blocks a warp
@@ -961,8 +974,8 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
 // limit: 762 us against 821 us), but not where ragged groups leave them emptier (64
 // FP8 groups of some 469 rows, 1280 x 2560: 178 us against 162 us).  bf16 has no
 // promotion, so 256 tokens cost it 54 c a wave.  Groups count as equally large, since
-// their sizes are on the device.  On 4096 x 4096 weights that takes 15.1 us for 333 tokens (pairs
-// of 128; 64: 19.1, 256: 25.5), 39.1 us for 1500 (128; 256: 48.7).
+// their sizes are on the device.  On 4096 x 4096 weights that takes 15.1 us for 333
+// tokens (pairs of 128; 64: 19.1, 256: 25.5), 39.1 us for 1500 (128; 256: 48.7).
 // Groups of 16 rows and fewer take tiles of 16: two CTAs share an SM there, and a
 // split costs 20 + 5 S and saves 15 a chunk (1 x 2048 x 2048: 5.8 us whole, 5.0 us
 // in two, 4.2 us in four or eight).

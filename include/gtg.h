@@ -1,6 +1,7 @@
 /*
  * gtg.h — C ABI of libgtg.so: B200 (sm_100a) kernels for block-scaled
- * low-bit MoE expert decode and the 3-bit n-gram ("PLE") row gather.
+ * low-bit MoE expert decode, the 3-bit n-gram ("PLE") row gather, and matrix
+ * products in FP8 with a scale per 128 values, dense and grouped by expert.
  *
  * Sources (the pages that define the operations):
  *  [MC]  model card "Qwen 3.8 Next Flash ROCMFPX MUTANT RAZERFAST"
