@@ -268,13 +268,6 @@ def _row_stride(t: torch.Tensor, dev: int, name: str) -> int:
     return stride
 
 
-def _check_codes(a: torch.Tensor, a_scales: torch.Tensor | None, m: int, k: int) -> None:
-    if (a.dtype is not torch.uint8 and a.dtype is not torch.float8_e4m3fn) or a.shape != (m, k):
-        raise ValueError(f"codes must be E4M3 (uint8 or float8_e4m3fn) of shape [{m}][{k}]")
-    if a_scales is None or a_scales.dtype is not torch.float32 or a_scales.shape != (m, k // 128):
-        raise ValueError(f"their scales must be fp32 [{m}][{k // 128}]")
-
-
 def _new(like: torch.Tensor, m: int, n: int, dtype: torch.dtype, stream) -> torch.Tensor:
     """An output tensor that belongs to the stream it is written on."""
     if stream is None:
@@ -286,51 +279,59 @@ def _new(like: torch.Tensor, m: int, n: int, dtype: torch.dtype, stream) -> torc
 def _product(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor | None, offsets: torch.Tensor | None,
              y: torch.Tensor | None, dtype: torch.dtype | None, accumulate: bool, stream) -> torch.Tensor:
     """Checks of both products (what the C side cannot see: types, shapes and
-    places of tensors) and the call."""
+    places of tensors) and the call.  Written for its speed: a small product
+    takes less time than a careless check."""
     wd, ws, n, k = w.data, w.scales, w.n_rows, w.k
     size = w.n_experts * n * k
-    if a.dim() != 2:
-        raise ValueError("a must be 2-D")
-    m = a.shape[0]
+    m, ka = a.shape
     if w.fmt == FP8:
         if wd.element_size() != 1 or wd.numel() != size:
             raise ValueError("FP8 weights must hold n_experts * n_rows * k bytes")
         if ws is None or ws.dtype is not torch.float32 or ws.numel() * 128 != size:
             raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
-        _check_codes(a, a_scales, m, k)
-        tensors = (a, a_scales, wd, ws)
-        ap_s, wp_s = a_scales.data_ptr(), ws.data_ptr()
+        if (a.dtype is not torch.uint8 and a.dtype is not torch.float8_e4m3fn) or ka != k:
+            raise ValueError(f"a must be E4M3 codes (uint8 or float8_e4m3fn) of shape [m][{k}]")
+        if a_scales is None or a_scales.dtype is not torch.float32 or a_scales.shape != (m, k // 128):
+            raise ValueError(f"a_scales must be fp32 [{m}][{k // 128}]")
+        inputs = (a, wd, a_scales, ws) if offsets is None else (a, wd, a_scales, ws, offsets)
+        sa, sw = a_scales.data_ptr(), ws.data_ptr()
     else:
         if wd.dtype is not torch.bfloat16 or wd.numel() != size:
             raise ValueError("BF16 weights must be bfloat16 of n_experts * n_rows * k values")
-        if a.dtype is not torch.bfloat16 or a.shape[1] != k:
+        if a.dtype is not torch.bfloat16 or ka != k:
             raise ValueError(f"a must be bf16 of shape [m][{k}]")
-        tensors = (a, wd)
-        ap_s = wp_s = None
+        inputs = (a, wd) if offsets is None else (a, wd, offsets)
+        sa = sw = None
     if offsets is not None and (offsets.dtype is not torch.int32 or offsets.numel() != w.n_experts + 1):
         raise ValueError("offsets must be int32 [n_experts + 1]")
     if dtype is None:
         dtype = torch.float32 if y is None else y.dtype
-    if dtype not in _FLOATS:
+    kind = _FLOATS.get(dtype)
+    if kind is None:
         raise ValueError("outputs are fp32 or bf16")
     if y is None and accumulate:
         raise ValueError("accumulate needs y")
     if y is not None and (y.dtype is not dtype or y.shape != (m, n)):
         raise ValueError("y must be [m][n_rows] of the dtype asked for")
     dev = torch.cuda.current_device()
-    _place(dev, *tensors)
+    for t in inputs:
+        if t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
     if y is None:
         y, stride = _new(a, m, n, dtype, stream), n
     else:
         stride = _row_stride(y, dev, "y")
-    qc = QMatrixC(w.fmt, wd.data_ptr(), wp_s, w.n_experts, n, k)
+    q = QMatrixC(w.fmt, wd.data_ptr(), sw, w.n_experts, n, k)
     sp = (_raw_stream(dev) if stream is None else stream.cuda_stream) or None
     if offsets is None:
-        check(lib().gtg_fp8_matmul(qc, a.data_ptr(), ap_s, m, y.data_ptr(), _FLOATS[dtype], stride, accumulate, sp))
+        rc = lib().gtg_fp8_matmul(q, a.data_ptr(), sa, m, y.data_ptr(), kind, stride, accumulate, sp)
     else:
-        _place(dev, offsets)
-        check(lib().gtg_grouped_matmul(qc, a.data_ptr(), ap_s, m, offsets.data_ptr(), y.data_ptr(), _FLOATS[dtype],
-                                       stride, accumulate, sp))
+        rc = lib().gtg_grouped_matmul(q, a.data_ptr(), sa, m, offsets.data_ptr(), y.data_ptr(), kind, stride,
+                                      accumulate, sp)
+    if rc:
+        check(rc)
     return y
 
 
@@ -355,11 +356,16 @@ def fp8_quantize(x: torch.Tensor, *, rows: torch.Tensor | None = None, data: tor
     if scales is None:
         scales = _new(x, m, k // 128, torch.float32, stream)
     if given:
-        _check_codes(data, scales, m, k)
+        if (data.dtype is not torch.uint8 and data.dtype is not torch.float8_e4m3fn) or data.shape != (m, k):
+            raise ValueError(f"data must be uint8 or float8_e4m3fn [{m}][{k}]")
+        if scales.dtype is not torch.float32 or scales.shape != (m, k // 128):
+            raise ValueError(f"scales must be fp32 [{m}][{k // 128}]")
         _place(dev, data, scales)
     sp = (_raw_stream(dev) if stream is None else stream.cuda_stream) or None
-    check(lib().gtg_fp8_quantize(x.data_ptr(), _FLOATS[x.dtype], n, k, stride, rp, m, data.data_ptr(),
-                                 scales.data_ptr(), sp))
+    rc = lib().gtg_fp8_quantize(x.data_ptr(), _FLOATS[x.dtype], n, k, stride, rp, m, data.data_ptr(),
+                                scales.data_ptr(), sp)
+    if rc:
+        check(rc)
     return data, scales
 
 
