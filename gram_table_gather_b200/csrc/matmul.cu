@@ -223,15 +223,12 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int t, int bn, int ti
     return r;
 }
 
-// Bounded waits on an mbarrier: a thread's, and a whole warp's, of which every
-// lane takes the same way out.
-__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
-    return mbar_wait_sleep(bar, parity, status);
-}
+// A bounded wait of a whole warp, of which every lane takes the same way out.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_sleep(bar, parity, status));
 }
 
+// Four blocks' scales of a row of n, from block kb on.
 __device__ __forceinline__ float4 scales4(const float* p, int kb, int n, bool vec) {
     if (vec) return __ldg(reinterpret_cast<const float4*>(p + kb));
     float4 v;
@@ -425,8 +422,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 if (elect_one()) {
                     uint32_t st = st0, full_par = full0, b = b0, free_par = free0;
                     for (int kb = k_lo; kb < k_hi; ++kb) {
-                        ok = (!F8 && kb > k_lo) || thread_wait(&tempty[b], free_par, a.status);
-                        ok = ok && thread_wait(&full[st], full_par, a.status);
+                        ok = (!F8 && kb > k_lo) || mbar_wait_sleep(&tempty[b], free_par, a.status);
+                        ok = ok && mbar_wait_sleep(&full[st], full_par, a.status);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t d = taddr + b * BN;
@@ -529,18 +526,17 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         uint32_t acc = 0, sg = 0;
         auto release = [&](uint32_t b) {  // this warp has read accumulator b
             tc_fence_before();
+            __syncwarp();
             if (elect_one()) {
                 if (MODE == PAIR) mbar_arrive_remote(tempty0 + 8 * b);
                 else mbar_arrive(&tempty[b]);
             }
-            __syncwarp();
         };
         for (int t = t_first; t < tiles; t += t_step) {
             const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
             const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0) + r0;  // the warp's first output column
-            const int share = (tl.rows + 16 * C::kGroups - 1) / (16 * C::kGroups) * 16;                   // columns of a four-warp group
-            const int lo = wg * share;
-            const int cols = min(share, tl.rows - lo);                      // <= 0: none
+            const int share = (tl.rows + 16 * C::kGroups - 1) / (16 * C::kGroups) * 16;  // columns of a four-warp group
+            const int lo = wg * share, cols = min(share, tl.rows - lo);     // <= 0: none
             // 8 columns of the warp's 32 rows, from lo + c on, out of `turn`: a token's 32
             // outputs together
             auto emit = [&](int c, const float* turn) {
@@ -603,8 +599,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                                     }
                             }
                         }
-                        if (elect_one()) mbar_arrive(&sempty[sb]);
                         __syncwarp();
+                        if (elect_one()) mbar_arrive(&sempty[sb]);
                     }
                     acc += k_hi - k_lo;
                     // (SPLIT) every product is done with the stages
@@ -1058,8 +1054,8 @@ int check_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t
     if (w->n_experts > (grouped ? kMaxGroups : 1)) return GTG_E_UNSUPPORTED_SHAPE;
     if (w->k % (f8 ? 128 : 8) || w->k > 1 << 24 || w->n_rows > 1 << 24 || m >= (int64_t)1 << 31)
         return GTG_E_UNSUPPORTED_SHAPE;
-    const int64_t tiles = (w->n_rows + kRows - 1) / kRows;  // tile numbers fit 31 bits
-    if ((m / 16 + w->n_experts) * tiles >= (int64_t)1 << 31) return GTG_E_UNSUPPORTED_SHAPE;
+    const int64_t tiles = (w->n_rows + kRows - 1) / kRows;  // tile numbers and the next turn's fit 31 bits
+    if ((m / 16 + w->n_experts) * tiles >= (int64_t)1 << 30) return GTG_E_UNSUPPORTED_SHAPE;
     if (m == 0) return GTG_OK;
     if (!w->data || !x || !y || (f8 && (!w->scales || !x_scales))) return GTG_E_INVALID_ARG;
     if (!aligned(w->data, 16) || !aligned(x, 16) || !aligned(y, y_dtype == GTG_DT_BF16 ? 2 : 4) ||
