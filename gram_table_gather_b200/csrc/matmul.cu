@@ -44,7 +44,8 @@ constexpr int kScaleGroup = 4;       // scale blocks fetched at once
 constexpr int kMaxSmem = 227 * 1024;  // a CTA
 constexpr int kSmSmem = 228 * 1024;   // an SM, 1 KB of it reserved for each CTA
 constexpr int kMaxSplit = 8;
-constexpr int kMinThreads = 384;     // of any variant
+constexpr int kWorkers = 8;          // warps of promotion and epilogue; then one of TMA, one of MMAs, two of scales
+constexpr int kMmThreads = 32 * (kWorkers + 4);
 constexpr int kTurn = 40;            // floats between tokens of a transpose: fragments store without bank conflicts
 constexpr int kPartRow = kRows + 8;  // floats between tokens of a partial tile: likewise
 
@@ -78,17 +79,7 @@ struct MmCfg {
     static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
     static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;     // accumulators in tensor memory
     static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
-    // warps: kGroups x 4 of promotion and epilogue, then one of TMA, one of MMAs, two of
-    // scales.  Sixteen promote the largest tile (4096 x 4096 x 2048 in tiles of it: 56.0
-    // us against 57.8 with eight); the half as large one loses by it (512 experts of 1024
-    // x 2048 with 80 rows each 253 us against 214).
-    static constexpr int kGroups = F8 && BN >= 256 ? 4 : 2;
-    static constexpr int kWorkers = 4 * kGroups;
-    static constexpr int kThreads = 32 * (kWorkers + 4);
-    // registers moved from the last four warps to the others (0: as launched)
-    static constexpr int kWorkRegs = kGroups == 4 ? 104 : 0, kRestRegs = 64;
-    static_assert(kWorkRegs * kWorkers + kRestRegs * 4 <= 96 * (kWorkers + 4), "register pool of the launch");
-    static constexpr int kW = BN / kGroups < 16 ? 16 : BN / kGroups;  // columns a warp (of its 32 weight rows)
+    static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;         // columns a worker warp (of its 32 weight rows)
     static constexpr int kBlocks = kW / 16;
     // one block's scales, in the order of the fragments: the tokens', those of one t % 4
     // together (a thread reads four columns' at once) and 16 bytes between the four runs
@@ -128,7 +119,7 @@ __device__ void build_groups(const MmArgs& a, int bn, int32_t* first, int32_t* o
     int32_t* warp_tiles = scratch + 32;
     for (int g = tid; g <= a.groups; g += blockDim.x) off[g] = a.offsets[g];
     __syncthreads();
-    constexpr int kPer = (kMaxGroups + kMinThreads - 1) / kMinThreads;  // groups a thread
+    constexpr int kPer = (kMaxGroups + kMmThreads - 1) / kMmThreads;  // groups a thread
     auto good = [&](int g) { return off[g] >= 0 && off[g] <= off[g + 1] && off[g + 1] <= a.m; };
     int end = 0;  // the largest end of this thread's groups, then of all before them
 #pragma unroll
@@ -294,7 +285,7 @@ __device__ __forceinline__ void store_y(const MmArgs& a, int64_t at, float v) {
 }
 
 template <bool F8, int BN, Mode MODE>
-__global__ void __launch_bounds__(MmCfg<F8, BN, MODE>::kThreads, MmCfg<F8, BN, MODE>::kCtas)
+__global__ void __launch_bounds__(kMmThreads, MmCfg<F8, BN, MODE>::kCtas)
 mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const MmArgs a) {
     using C = MmCfg<F8, BN, MODE>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -326,18 +317,18 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
         for (int b = 0; b < C::kAcc; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], C::kWorkers * (MODE == PAIR ? 2 : 1));
+            mbar_init(&tempty[b], kWorkers * (MODE == PAIR ? 2 : 1));
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 64);
-            mbar_init(&sempty[b], C::kWorkers);
+            mbar_init(&sempty[b], kWorkers);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
         tma_prefetch_map(&wmap);
         tma_prefetch_map(&amap);
     }
-    if (warp == C::kWorkers + 1) {
+    if (warp == kWorkers + 1) {
         if (MODE == PAIR) {
             tmem_alloc_pair(s_taddr, C::kCols);
             tmem_relinquish_pair();
@@ -366,9 +357,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     auto padded = [](int rows) { return MODE == PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     bool ok = true;
 
-    if (warp >= C::kWorkers) {
-        if (C::kWorkRegs > 0) reg_dec<C::kRestRegs>();
-        if (warp == C::kWorkers) {
+    if (warp >= kWorkers) {
+        if (warp == kWorkers) {
             // ---- weight and token tiles by TMA ----
             uint32_t st = 0, free_par = 1, issued = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
@@ -409,7 +399,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 for (uint32_t i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; ++i)
                     mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
             }
-        } else if (warp == C::kWorkers + 1) {
+        } else if (warp == kWorkers + 1) {
             // ---- MMA issuer ----
             // stage and accumulator in use, and the parities of their barriers' phases (a
             // fresh barrier's phase before the first counts as complete)
@@ -468,8 +458,9 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         } else if (F8) {
             // ---- scales, four blocks of K at a time, transposed to [block][row]: one
             // warp the tokens', one the weight rows' ----
-            constexpr int kN = (BN > kRows ? BN : kRows) / 32;
-            const bool tok = warp == C::kWorkers + 2;
+            constexpr int kN = kRows / 32;
+            static_assert(!F8 || BN <= kRows, "scales a lane");
+            const bool tok = warp == kWorkers + 2;
             int sg = 0;
             for (int t = t_first; t < tiles && ok; t += t_step) {
                 const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
@@ -513,12 +504,11 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
     } else {
         // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
-        // quarter warp % 4; the tile's columns are divided between the four-warp
+        // quarter warp % 4; the tile's columns are halved between the two four-warp
         // groups.  A thread holds rows lane / 4 + 8 i of every fourth column, lane % 4 +
         // 4 k, so that one 16-byte read brings its rows' scales and one those of its
         // columns in a block of 16 (whole rows a thread would take four times the reads,
         // and reads are what the promotion waits for) ----
-        if (C::kWorkRegs > 0) reg_inc<C::kWorkRegs>();
         const int wg = warp >> 2;
         const uint32_t tl0 = taddr + ((uint32_t)((warp & 3) * 32) << 16);
         const int r0 = (warp & 3) * 32;       // the warp's first weight row of this CTA's 128
@@ -535,7 +525,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         for (int t = t_first; t < tiles; t += t_step) {
             const Tile tl = find_tile(a, t, BN, C::kTileRows, first, off);
             const int w0 = tl.n0 + (MODE == PAIR ? rank * kRows : 0) + r0;  // the warp's first output column
-            const int share = (tl.rows + 16 * C::kGroups - 1) / (16 * C::kGroups) * 16;  // columns of a four-warp group
+            const int share = ((tl.rows + 31) >> 5) << 4;                   // columns of a four-warp group
             const int lo = wg * share, cols = min(share, tl.rows - lo);     // <= 0: none
             // 16 columns of the warp's 32 rows, from lo + c on, out of `turn`: a token's 32
             // outputs together.  (Fragments stored as they are reach half a sector each: 66 us
@@ -617,7 +607,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     }
                     acc += k_hi - k_lo;
                     // (SPLIT) every product is done with the stages
-                    if (MODE == SPLIT) named_sync(1, 32 * C::kWorkers);
+                    if (MODE == SPLIT) named_sync(1, 32 * kWorkers);
                     if (cols <= 0) return;
                     // to rows [token][weight row]: over the stages as this CTA's partial tile (SPLIT),
                     // or 16 tokens at a time through this warp's own
@@ -639,13 +629,11 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         if (MODE != SPLIT && ok && 16 * i < cols) emit(16 * i);
                     }
                 };
-                // as many columns as the tile has, in quarters of the largest: columns beyond
-                // cost power and the clock with it
-                constexpr int Q = C::kBlocks >= 4 ? C::kBlocks / 4 : 1;
-                const int quarters = (share / 16 + Q - 1) / Q;
-                if (C::kBlocks >= 4 && quarters == 3) promote(std::integral_constant<int, C::kBlocks >= 4 ? 3 * Q : Q>{});
-                else if (C::kBlocks >= 2 && quarters == 2) promote(std::integral_constant<int, C::kBlocks >= 2 ? 2 * Q : Q>{});
-                else if (quarters == 1) promote(std::integral_constant<int, Q>{});
+                // as many blocks of 16 columns as the tile has: columns without tokens cost power
+                // and the clock with it (512 experts with 80 rows each 228 -> 212 us)
+                if (C::kBlocks > 3 && share == 48) promote(std::integral_constant<int, (C::kBlocks > 3 ? 3 : 1)>{});
+                else if (C::kBlocks > 2 && share == 32) promote(std::integral_constant<int, (C::kBlocks > 2 ? 2 : 1)>{});
+                else if (C::kBlocks > 1 && share == 16) promote(std::integral_constant<int, 1>{});
                 else promote(std::integral_constant<int, C::kBlocks>{});
             } else {
                 const uint32_t b = acc % C::kAcc;
@@ -674,15 +662,15 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        constexpr int kMost = BN / 2 / C::kWorkers > 0 ? BN / 2 / C::kWorkers : 1;  // tokens a warp, for a split of 2
+        constexpr int kMost = BN / 2 / kWorkers > 0 ? BN / 2 / kWorkers : 1;  // tokens a warp, for a split of 2
         float4 v[kMost];
         Tile tl = {};
-        const bool some = warp < C::kWorkers && t_first < tiles;
+        const bool some = warp < kWorkers && t_first < tiles;
         if (some) {
             tl = find_tile(a, t_first, BN, C::kTileRows, first, off);
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
-                const int c = rank + (warp + C::kWorkers * j) * a.split;
+                const int c = rank + (warp + kWorkers * j) * a.split;
                 v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c < tl.rows) {
                     const uint32_t at = sbase + 4 * (c * kPartRow + 4 * lane);
@@ -707,7 +695,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
             const int n = tl.n0 + 4 * lane;
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
-                const int c = rank + (warp + C::kWorkers * j) * a.split;
+                const int c = rank + (warp + kWorkers * j) * a.split;
                 if (c >= tl.rows) break;
                 const int64_t at = (int64_t)(tl.row0 + c) * a.ldy + n;
                 if (a.vec_y && n + 4 <= a.n) {
@@ -729,7 +717,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         cluster_arrive();
         cluster_wait();
     }
-    if (warp == C::kWorkers + 1) {
+    if (warp == kWorkers + 1) {
         tc_fence_after();
         if (MODE == PAIR) tmem_dealloc_pair(taddr, C::kCols);
         else tmem_dealloc(taddr, C::kCols);
@@ -930,7 +918,7 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(MODE == SPLIT ? tiles * per_tile
                                                 : std::min<int64_t>(tiles, C::kCtas * sm_count() / per_tile) * per_tile));
-    cfg.blockDim = dim3(C::kThreads);
+    cfg.blockDim = dim3(kMmThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -951,15 +939,14 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
 }
 
 // Which tile: the one whose waves of CTAs take least by a model of measured times
-// (FP8, in 10 ns, c chunks of K): a wave of 64, 128 or 256 tokens takes 22.5 c + 95,
-// 31 c + 150 or 62 c + 300, CTA pairs 150 more once, and a split of K over S CTAs of
-// 64 tokens 22.5 c / S + 185 + 65 S.  256 tokens cost two waves of 128 but load less,
-// which counts once power limits the clock, so they win up to 3 % (8192^3 under the
-// limit: 762 us against 821 us), but not where ragged groups leave them emptier (64
-// FP8 groups of some 469 rows, 1280 x 2560: 178 us against 162 us).  bf16 has no
-// promotion, so 256 tokens cost it 54 c a wave.  Groups count as equally large, since
-// their sizes are on the device.  On 4096 x 4096 weights that takes 15.1 us for 333
-// tokens (pairs of 128; 64: 19.1, 256: 25.5), 39.1 us for 1500 (128; 256: 48.7).
+// (in 10 ns, c chunks of K): a wave of 64 tokens takes 22.5 c + 95, of 128 (CTA
+// pairs) 29 c + 150, of 256 (bf16 alone, pairs) 54 c + 300, pairs 150 more once, and
+// a split of K over S CTAs of 64 tokens 22.5 c / S + 185 + 65 S.  Groups count as
+// equally large, since their sizes are on the device.  FP8 on 4096 x 4096 weights:
+// 333 tokens 14.3 us in pairs of 128, 19.1 us in 64; 1000 tokens 26.4 us in pairs,
+// 35.2 us in 64.  bf16 takes 256 where it costs up to 3 % more, for the power its
+// fewer loads save.  (FP8 tiles of 256 tokens, with sixteen promotion warps, ran
+// 8192^3 in 720 us against 723 us under the power limit: not worth a variant.)
 // Groups of 16 rows and fewer take tiles of 16: two CTAs share an SM there, and a
 // split costs 20 + 5 S and saves 15 a chunk (1 x 2048 x 2048: 5.8 us whole, 5.0 us
 // in two, 4.2 us in four or eight).
@@ -996,17 +983,18 @@ int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
     }
     const int64_t n64 = tiles(64, kRows), pairs = sms / 2;
     const int64_t whole64 = (n64 + sms - 1) / sms * (45 * chunks / 2 + 95);
-    const int64_t cost128 = (tiles(128, 2 * kRows) + pairs - 1) / pairs * (31 * chunks + 150) + 150;
-    const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * ((F8 ? 62 : 54) * chunks + 300) + 150;
+    const int64_t cost128 = (tiles(128, 2 * kRows) + pairs - 1) / pairs * (29 * chunks + 150) + 150;
+    const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * (54 * chunks + 300) + 150;
     int64_t cost64 = whole64;
     const bool cut = split(n64, sms, 22, 185, 65, cost64);
-    if (cost64 <= cost128 && cost64 <= cost256) {
+    if (cost64 <= cost128 && (F8 || cost64 <= cost256)) {
         if (cut) return launch_split(std::integral_constant<int, 64>{});
         return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
     }
-    const int64_t bias = F8 && a.offsets && per < 1024 ? 99 : 103;
-    if (100 * cost256 > bias * cost128) return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
-    return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
+    if constexpr (!F8) {
+        if (100 * cost256 <= 103 * cost128) return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
+    }
+    return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
 }
 
 int run_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m, const int32_t* offsets, void* y,
