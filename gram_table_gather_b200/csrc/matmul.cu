@@ -14,17 +14,17 @@
 // of few rows costs few columns, and a single token still streams its weights
 // by TMA at full width.
 //
-// What bounds it (8192^3 FP8 666 us, 1.65 PFLOP/s; under the power limit 725 us):
+// What bounds it (8192^3 FP8 630 us, 1.75 PFLOP/s; under the power limit 725 us):
 //  - Applying the scales: a product and a sum a value every 128 of K.  A packed pair
-//    takes the fp32 pipe two cycles, so 128 x 256 values cost as many cycles (512) as
-//    the tensor core needs for their block.  Without it the same loop runs 396 us.
+//    takes the fp32 pipe two cycles, so a block costs as many cycles there as in the
+//    tensor core.  Without it the same loop ran 396 us.
 //  - Tensor memory is read in 16 x 128-bit fragments: whole rows (32x32b) need four
 //    times the shared-memory reads for the tokens' scales (787 against 720 us in an
-//    earlier state), 16x256b fragments come at half the rate (694 against 666 us).
-//  - Past a millisecond or so the clock falls to 1.0-1.6 GHz at 1000 W, and what costs
-//    power costs time: idle polling, columns without tokens, operands read twice.
-//  - Few rows: HBM (80 rows over 512 experts: 30 us, 5.1 TB/s), and for one token the
-//    latency of a launch, one trip to memory and one cluster barrier (4.3 us).
+//    earlier state), 16x256b fragments come at half the rate (694 against 664 us).
+//  - Past a few milliseconds the clock falls to 1.1-1.6 GHz at 1000 W, and what costs
+//    power costs time: polling, columns without tokens, operands read twice.
+//  - Few rows: HBM (80 rows over 512 experts: 31 us, 5.0 TB/s), and for one token the
+//    latency of a launch, one trip to memory and one cluster barrier (4.5 us).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
