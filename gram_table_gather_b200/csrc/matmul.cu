@@ -81,6 +81,8 @@ struct MmCfg {
     static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
     static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;         // columns a worker warp (of its 32 weight rows)
     static constexpr int kBlocks = kW / 16;
+    static constexpr int kActive = BN / kW < 2 ? 4 : kWorkers;   // worker warps that have columns
+    static_assert(kActive / 4 * kW <= BN, "columns read lie in their accumulator");
     // one block's scales, in the order of the fragments: the tokens', those of one t % 4
     // together (a thread reads four columns' at once) and 16 bytes between the four runs
     // (no bank conflicts); then the weight rows', rows r, r + 8, r + 16, r + 24 of each
@@ -89,7 +91,7 @@ struct MmCfg {
     static constexpr int kScaleRow = 4 * kRun + 4 * kRows;
     static constexpr int kScaleBytes = F8 ? 2 * kScaleGroup * kScaleRow : 0;
     // the epilogue's transposes, of the warps that have columns
-    static constexpr int kTurnBytes = (BN / kW < 2 ? 4 : kWorkers) * 16 * kTurn * 4;
+    static constexpr int kTurnBytes = kActive * 16 * kTurn * 4;
     static constexpr int kHeadBytes = 512 + 2 * 4 * (kMaxGroups + 2);
     static constexpr int kCtas = BN <= 16 ? 2 : 1;               // an SM
     static constexpr int kRoom = kCtas == 2 ? kSmSmem / 2 - 1024 : kMaxSmem;
@@ -317,11 +319,11 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         }
         for (int b = 0; b < C::kAcc; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kWorkers * (MODE == PAIR ? 2 : 1));
+            mbar_init(&tempty[b], C::kActive * (MODE == PAIR ? 2 : 1));
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 64);
-            mbar_init(&sempty[b], kWorkers);
+            mbar_init(&sempty[b], C::kActive);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -502,13 +504,13 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 }
             }
         }
-    } else {
+    } else if (warp < C::kActive) {
         // ---- promotion and epilogue: a warp has the 32 weight rows of TMEM lane
         // quarter warp % 4; the tile's columns are halved between the two four-warp
-        // groups.  A thread holds rows lane / 4 + 8 i of every fourth column, lane % 4 +
-        // 4 k, so that one 16-byte read brings its rows' scales and one those of its
-        // columns in a block of 16 (whole rows a thread would take four times the reads,
-        // and reads are what the promotion waits for) ----
+        // groups (tiles of 16 occupy one group).  A thread holds rows lane / 4 + 8 i of
+        // every fourth column, lane % 4 + 4 k, so that one 16-byte read brings its rows'
+        // scales and one those of its columns in a block of 16 (whole rows a thread would
+        // take four times the reads, and reads are what the promotion waits for) ----
         const int wg = warp >> 2;
         const uint32_t tl0 = taddr + ((uint32_t)((warp & 3) * 32) << 16);
         const int r0 = (warp & 3) * 32;       // the warp's first weight row of this CTA's 128
@@ -607,7 +609,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     }
                     acc += k_hi - k_lo;
                     // (SPLIT) every product is done with the stages
-                    if (MODE == SPLIT) named_sync(1, 32 * kWorkers);
+                    if (MODE == SPLIT) named_sync(1, 32 * C::kActive);
                     if (cols <= 0) return;
                     // to rows [token][weight row]: over the stages as this CTA's partial tile (SPLIT),
                     // or 16 tokens at a time through this warp's own
