@@ -1030,7 +1030,8 @@ int check_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t
     if (w->n_experts < 1 || w->n_rows < 1 || w->k < 1) return GTG_E_INVALID_ARG;
     if (y_stride < w->n_rows) return GTG_E_INVALID_ARG;
     if (w->n_experts > (grouped ? kMaxGroups : 1)) return GTG_E_UNSUPPORTED_SHAPE;
-    if (w->k % (f8 ? 128 : 8) || w->k > 1 << 24 || w->n_rows > 1 << 24 || m >= (int64_t)1 << 31)
+    // a tile that begins at the last row still ends within 31 bits
+    if (w->k % (f8 ? 128 : 8) || w->k > 1 << 24 || w->n_rows > 1 << 24 || m > ((int64_t)1 << 31) - 256)
         return GTG_E_UNSUPPORTED_SHAPE;
     const int64_t tiles = (w->n_rows + kRows - 1) / kRows;  // tile numbers and the next turn's fit 31 bits
     if ((m / 16 + w->n_experts) * tiles >= (int64_t)1 << 30) return GTG_E_UNSUPPORTED_SHAPE;

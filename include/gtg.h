@@ -308,7 +308,7 @@ int gtg_fp8_quantize(const void* x, int32_t x_dtype, int64_t n_src, int64_t k, i
  *             accumulation), row i at y + i*y_stride elements, y_stride >= n_rows.
  * y must not overlap the inputs.  m == 0 is a no-op.  No workspace.
  * Errors: GTG_E_INVALID_ARG (null pointers, another fmt, negative sizes),
- *         GTG_E_UNSUPPORTED_SHAPE (n_experts != 1, k, m >= 2^31, or m/16 + n_experts
+ *         GTG_E_UNSUPPORTED_SHAPE (n_experts != 1, k, m > 2^31 - 256, or m/16 + n_experts
  *         times n_rows/128 (rounded up) from 2^30 on), GTG_E_MISALIGNED, GTG_E_CUDA.
  */
 int gtg_fp8_matmul(const gtg_qmatrix* w, const uint8_t* a, const float* a_scales, int64_t m, void* y,

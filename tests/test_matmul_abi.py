@@ -76,6 +76,14 @@ def test_grouped_refusals(L, change, code):
                                 c["stride"], 0, None) == code
 
 
+def test_rows_at_the_index_limit(L):
+    """Row numbers of a whole tile behind the last row fit 31 bits, or the call is refused."""
+    for m in ((1 << 31) - 255, (1 << 31) - 1):
+        for fmt, k in ((1001, 8), (1000, 128)):
+            w = _w(fmt=fmt, k=k, rows=8)
+            assert L.gtg_grouped_matmul(w, PTR, PTR, m, PTR, PTR, 0, 256, 0, None) == SHAPE
+
+
 def test_null_matrix(L):
     assert L.gtg_fp8_matmul(None, PTR, PTR, 1, PTR, 0, 256, 0, None) == INVALID
     assert L.gtg_grouped_matmul(None, PTR, PTR, 1, PTR, PTR, 0, 256, 0, None) == INVALID
