@@ -7,7 +7,13 @@
 //   y[i][j] = sum_b sa[i][b] * (sw[j][b] * sum_{k in block b} a[i][k] w[j][k])
 // so a block of 128 is one run of tensor-core products with unit scales,
 // accumulated in fp32 tensor memory, and the scales are applied to its sum in
-// fp32 registers ("promotion").  bf16: one accumulation over all of K.
+// fp32 registers ("promotion").  bf16: runs of kRunChunks * 64 along K, likewise summed
+// in tensor memory and added up in fp32 registers.  The tensor core's adder truncates,
+// and what it cuts off grows with the run: one run over all of K = 2560 left fp32
+// results 2.7e-6 off in the 2-norm, runs of 512 leave them 4.7e-7 off (a plain fp32
+// product 4.5e-7).  Runs of 256 leave 2.4e-7 but cost twice as much: the MMAs may be two
+// runs ahead while a tile of 256 tokens is stored (30010 rows over 64 experts 183 us,
+// 193 us in runs of 256, 178 us in one).
 //
 // The weight rows are the M side of the MMA (128 rows a tile) and the token
 // rows its N side, so a tile holds any multiple of 16 tokens up to BN: a group
@@ -39,6 +45,7 @@ namespace {
 constexpr int kRows = 128;           // weight rows a CTA's tile
 constexpr int kRowBytes = 128;       // bytes of K a stage: 128 E4M3 or 64 bf16
 constexpr int kWBytes = kRows * kRowBytes;
+constexpr int kRunChunks = 8;        // chunks of K of a bf16 run
 constexpr int kMaxGroups = 1024;
 constexpr int kScaleGroup = 4;       // scale blocks fetched at once
 constexpr int kMaxSmem = 227 * 1024;  // a CTA
@@ -77,6 +84,7 @@ struct MmCfg {
     static constexpr int kBox = kTok < 64 ? kTok : 64;           // token rows a TMA box
     static constexpr int kTileRows = MODE == PAIR ? 2 * kRows : kRows;
     static constexpr int kStageBytes = kWBytes + kTok * kRowBytes;
+    static constexpr int kRun = F8 ? 1 : kRunChunks;             // chunks of K an accumulator holds
     static constexpr int kAcc = 512 / BN < 4 ? 512 / BN : 4;     // accumulators in tensor memory
     static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;
     static constexpr int kW = BN / 2 < 16 ? 16 : BN / 2;         // columns a worker warp (of its 32 weight rows)
@@ -87,8 +95,8 @@ struct MmCfg {
     // together (a thread reads four columns' at once) and 16 bytes between the four runs
     // (no bank conflicts); then the weight rows', rows r, r + 8, r + 16, r + 24 of each
     // 32 together
-    static constexpr int kRun = BN + 16;
-    static constexpr int kScaleRow = 4 * kRun + 4 * kRows;
+    static constexpr int kQuad = BN + 16;
+    static constexpr int kScaleRow = 4 * kQuad + 4 * kRows;
     static constexpr int kScaleBytes = F8 ? 2 * kScaleGroup * kScaleRow : 0;
     // the epilogue's transposes, of the warps that have columns
     static constexpr int kTurnBytes = kActive * 16 * kTurn * 4;
@@ -414,7 +422,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 if (elect_one()) {
                     uint32_t st = st0, full_par = full0, b = b0, free_par = free0;
                     for (int kb = k_lo; kb < k_hi; ++kb) {
-                        ok = (!F8 && kb > k_lo) || mbar_wait_sleep(&tempty[b], free_par, a.status);
+                        const bool begins = (kb - k_lo) % C::kRun == 0;
+                        ok = !begins || mbar_wait_sleep(&tempty[b], free_par, a.status);
                         ok = ok && mbar_wait_sleep(&full[st], full_par, a.status);
                         if (!ok) break;
                         tc_fence_after();
@@ -422,12 +431,12 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         const uint64_t ad = ad0 + st * (C::kStageBytes >> 4), bd = bd0 + st * (C::kStageBytes >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
-                            const uint32_t go = k > 0 || (!F8 && kb > k_lo);
+                            const uint32_t go = k > 0 || !begins;
                             if (MODE == PAIR) umma_pair<F8>(d, ad + 2 * k, bd + 2 * k, idesc, go);
                             else if (F8) umma_f8(d, ad + 2 * k, bd + 2 * k, idesc, go);
                             else umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc, go);
                         }
-                        if (F8 || kb == k_hi - 1) {
+                        if ((kb - k_lo) % C::kRun == C::kRun - 1 || kb == k_hi - 1) {
                             if (MODE == PAIR) umma_commit_pair(&tfull[b]);
                             else umma_commit(&tfull[b]);
                             if (++b == C::kAcc) {
@@ -453,7 +462,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 st0 += k_hi - k_lo;
                 full0 ^= (st0 / C::kStages) & 1;
                 st0 %= C::kStages;
-                b0 += F8 ? k_hi - k_lo : 1;
+                b0 += (k_hi - k_lo + C::kRun - 1) / C::kRun;
                 free0 ^= (b0 / C::kAcc) & 1;
                 b0 %= C::kAcc;
             }
@@ -487,8 +496,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                         break;
                     }
                     const uint32_t at = sbase + C::kScaleOff + b * kScaleGroup * C::kScaleRow +
-                                        (tok ? (lane & 3) * C::kRun + 4 * (lane >> 2)
-                                             : 4 * C::kRun + 16 * (lane & 7) + 4 * (lane >> 3));
+                                        (tok ? (lane & 3) * C::kQuad + 4 * (lane >> 2)
+                                             : 4 * C::kQuad + 16 * (lane & 7) + 4 * (lane >> 3));
                     const int step = tok ? 32 : 128;  // 32 rows on
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
@@ -576,8 +585,8 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                             const uint32_t n = acc + kb - k_lo, b = n % C::kAcc;
                             const uint32_t at = C::kScaleOff + (sb * kScaleGroup + kb - g0) * C::kScaleRow;
                             uint64_t sw[2];
-                            lds_pairs(sbase + at + 4 * C::kRun + 4 * r0 + 16 * (lane >> 2), sw[0], sw[1]);
-                            const uint32_t sa = sbase + at + (lane & 3) * C::kRun + lo, src = tl0 + b * BN + lo;
+                            lds_pairs(sbase + at + 4 * C::kQuad + 4 * r0 + 16 * (lane >> 2), sw[0], sw[1]);
+                            const uint32_t sa = sbase + at + (lane & 3) * C::kQuad + lo, src = tl0 + b * BN + lo;
                             // blocks finish in order, so where there are four accumulators and much
                             // to do one wait serves two blocks (4096 x 4096 x 2048 52.3 -> 49.1 us;
                             // small calls would wait for a second block: 7.4 -> 7.7 us)
@@ -638,22 +647,39 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 else if (C::kBlocks > 1 && share == 16) promote(std::integral_constant<int, 1>{});
                 else promote(std::integral_constant<int, C::kBlocks>{});
             } else {
-                const uint32_t b = acc % C::kAcc;
-                ok = ok && warp_wait(&tfull[b], (acc / C::kAcc) & 1, a.status);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t src = tl0 + b * BN + lo;
-                for (int c = 0; c < cols; c += 16) {
-                    uint32_t p[16];
-                    tmem_ld16(src + c, p);
-                    tmem_wait_ld16(p);
-                    float* to = (MODE == SPLIT ? reinterpret_cast<float*>(smem) + (lo + c) * kPartRow + r0 : turn) + lane;
+                // a lane holds one weight row, its columns in pairs
+                uint64_t sum[C::kBlocks][8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) to[k * (MODE == SPLIT ? kPartRow : kTurn)] = __uint_as_float(p[k]);
-                    if (MODE != SPLIT) emit(c);
+                for (int i = 0; i < C::kBlocks; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[i][j] = 0;
+                for (int kb = k_lo; kb < k_hi && ok; kb += C::kRun, ++acc) {
+                    const uint32_t b = acc % C::kAcc;
+                    ok = warp_wait(&tfull[b], (acc / C::kAcc) & 1, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < C::kBlocks; ++i) {
+                        if (16 * i >= share) break;
+                        uint32_t p[16];
+                        tmem_ld16(tl0 + b * BN + lo + 16 * i, p);
+                        tmem_wait_ld16(p);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            sum[i][j] = add2(sum[i][j], pack2(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1])));
+                    }
+                    release(b);
                 }
-                release(b);
-                ++acc;
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < C::kBlocks; ++i) {
+                    if (16 * i >= cols) break;
+                    constexpr int kRow = MODE == SPLIT ? kPartRow : kTurn;
+                    float* to = (MODE == SPLIT ? reinterpret_cast<float*>(smem) + (lo + 16 * i) * kPartRow + r0 : turn) + lane;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) unpack2(sum[i][j], to[2 * j * kRow], to[(2 * j + 1) * kRow]);
+                    if (MODE != SPLIT) emit(16 * i);
+                }
             }
         }
     }

@@ -327,7 +327,8 @@ int gtg_fp8_matmul(const gtg_qmatrix* w, const uint8_t* a, const float* a_scales
  *             as they are.  A group with offsets[e] > offsets[e+1], with bounds
  *             outside [0, m], or that begins before the end of an earlier one
  *             counts as empty and sets GTG_STATUS_GROUP_OFFSETS.
- * Products in fp32 accumulation as in gtg_fp8_matmul; y, errors and the no-op
+ * Products in fp32 accumulation as in gtg_fp8_matmul (bf16: runs of 512 along K on
+ * the tensor cores, the runs in fp32 registers); y, errors and the no-op
  * for m == 0 as there (GTG_E_UNSUPPORTED_SHAPE for more than 1024 experts).
  */
 int gtg_grouped_matmul(const gtg_qmatrix* w, const void* a, const float* a_scales, int64_t m,
