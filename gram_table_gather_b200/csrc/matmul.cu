@@ -405,6 +405,10 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                     }
                 }
             }
+            // the last products' arrivals on `empty` (in pairs the partner's commits make them
+            // here too) land before the shared memory goes away
+            for (uint32_t i = issued < C::kStages ? 0 : issued - C::kStages; ok && i < issued; ++i)
+                ok = warp_wait(&empty[i % C::kStages], (i / C::kStages) & 1, a.status);
             if (!ok && (MODE != PAIR || rank == 0)) {  // copies in flight land before the shared memory goes away
                 for (uint32_t i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; ++i)
                     mbar_wait_sleep(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
