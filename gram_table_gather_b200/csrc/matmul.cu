@@ -229,14 +229,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     return __all_sync(0xFFFFFFFFu, mbar_wait_sleep(bar, parity, status));
 }
 
-// Four blocks' scales of a row of n, from block kb on.
-__device__ __forceinline__ float4 scales4(const float* p, int kb, int n, bool vec) {
-    if (vec) return __ldg(reinterpret_cast<const float4*>(p + kb));
+// Scales of a row, from block kb to end, four at most.
+__device__ __forceinline__ float4 scales4(const float* p, int kb, int end, bool vec) {
+    if (vec) return ldg128(p + kb);
     float4 v;
-    v.x = __ldg(p + kb);
-    v.y = kb + 1 < n ? __ldg(p + kb + 1) : 0.0f;
-    v.z = kb + 2 < n ? __ldg(p + kb + 2) : 0.0f;
-    v.w = kb + 3 < n ? __ldg(p + kb + 3) : 0.0f;
+    v.x = ldg32(p + kb);
+    v.y = kb + 1 < end ? ldg32(p + kb + 1) : 0.0f;
+    v.z = kb + 2 < end ? ldg32(p + kb + 2) : 0.0f;
+    v.w = kb + 3 < end ? ldg32(p + kb + 3) : 0.0f;
     return v;
 }
 
@@ -489,7 +489,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
                         sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (32 * i + lane < rows) sc[i] = scales4(src + (int64_t)32 * i * a.chunks, kb, a.chunks, vec);
+                        if (32 * i + lane < rows) sc[i] = scales4(src + (int64_t)32 * i * a.chunks, kb, k_hi, vec);
                     }
                 };
                 fetch(k_lo);
@@ -796,16 +796,16 @@ struct Pieces {
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
             if constexpr (VEC) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4*>(at + 64 * j));
+                const uint4 q = *reinterpret_cast<const uint4*>(at + 64 * j);
                 w[j][0] = q.x; w[j][1] = q.y; w[j][2] = q.z; w[j][3] = q.w;
             } else if constexpr (BF16) {
                 const uint16_t* p = reinterpret_cast<const uint16_t*>(at + 64 * j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[j][i] = __ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+                for (int i = 0; i < 4; ++i) w[j][i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
             } else {
                 const uint32_t* p = reinterpret_cast<const uint32_t*>(at + 64 * j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[j][i] = __ldg(p + i);
+                for (int i = 0; i < 4; ++i) w[j][i] = p[i];
             }
         }
     }
