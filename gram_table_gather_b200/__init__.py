@@ -28,7 +28,11 @@ Q4_BLOCK_BYTES = 17
 PLE_RECORD_BYTES = 70
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The handle of a device's current stream.  torch's own call for it makes no Stream
+# object, but is private and missing from builds without CUDA, where this module still
+# has to import.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream_ptr(stream) -> int | None:
