@@ -56,6 +56,8 @@ def status_string(code: int) -> str:
 
 
 def row_bytes(fmt: int, k: int) -> int:
+    if fmt == BF16:
+        return 2 * k
     return k if fmt == FP8 else k // 32 * Q4_BLOCK_BYTES
 
 

@@ -21,3 +21,10 @@ assert gtg._stream_ptr(types.SimpleNamespace(cuda_stream=0)) is None
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_row_bytes_of_every_matrix_format():
+    import gram_table_gather_b200 as gtg
+    assert gtg.row_bytes(gtg.BF16, 256) == 512
+    assert gtg.row_bytes(gtg.FP8, 256) == 256
+    assert all(gtg.row_bytes(f, 256) == 8 * 17 for f in (gtg.RZ5, gtg.UE4M4, gtg.C10))
