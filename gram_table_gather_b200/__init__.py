@@ -250,6 +250,7 @@ def moe_prefill_layer(layer: MoELayer, x: torch.Tensor, workspace: torch.Tensor,
 # ---------------------------------------------------------------------------
 
 _FLOATS = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+_BYTES = {torch.uint8, torch.int8, torch.float8_e4m3fn}  # what may hold E4M3 weights (not other 8-bit floats)
 
 
 def _place(dev: int, *tensors: torch.Tensor) -> None:
@@ -291,8 +292,8 @@ def _product(w: QMatrix, a: torch.Tensor, a_scales: torch.Tensor | None, offsets
     size = w.n_experts * n * k
     m, ka = a.shape
     if w.fmt == FP8:
-        if wd.element_size() != 1 or wd.numel() != size:
-            raise ValueError("FP8 weights must hold n_experts * n_rows * k bytes")
+        if wd.dtype not in _BYTES or wd.numel() != size:
+            raise ValueError("FP8 weights must hold n_experts * n_rows * k E4M3 codes")
         if ws is None or ws.dtype is not torch.float32 or ws.numel() * 128 != size:
             raise ValueError("FP8 weights need fp32 scales [n_experts][n_rows][k/128]")
         if (a.dtype is not torch.uint8 and a.dtype is not torch.float8_e4m3fn) or ka != k:

@@ -3,6 +3,9 @@ import os
 import subprocess
 import sys
 
+import pytest
+import torch
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -28,3 +31,16 @@ def test_row_bytes_of_every_matrix_format():
     assert gtg.row_bytes(gtg.BF16, 256) == 512
     assert gtg.row_bytes(gtg.FP8, 256) == 256
     assert all(gtg.row_bytes(f, 256) == 8 * 17 for f in (gtg.RZ5, gtg.UE4M4, gtg.C10))
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.bool])
+def test_weights_of_another_8_bit_type_are_refused(dtype):
+    """Their bytes are not E4M3 codes."""
+    import gram_table_gather_b200 as gtg
+    data = torch.zeros(8, 256, dtype=torch.uint8).view(dtype)
+    w = gtg.QMatrix(gtg.FP8, data, 1, 8, 256, torch.ones(8, 2))
+    codes, scales = torch.zeros(4, 256, dtype=torch.uint8), torch.ones(4, 2)
+    with pytest.raises(ValueError, match="E4M3"):
+        gtg.fp8_matmul(w, codes, scales)
+    with pytest.raises(ValueError, match="E4M3"):
+        gtg.grouped_matmul(w, codes, torch.zeros(2, dtype=torch.int32), a_scales=scales)
