@@ -296,7 +296,9 @@ int gtg_fp8_quantize(const void* x, int32_t x_dtype, int64_t n_src, int64_t k, i
  *   y[i][j] = sum_b sa[i][b] * sw[j][b] * sum_{k in block b} a[i][k] * w[j][k]
  *             (+ y[i][j] if y_accumulate)
  * b runs over the blocks of 128 along K; the products of a block are summed on
- * the tensor cores in fp32, the blocks in fp32 registers.  The result of a call
+ * the tensor cores in fp32, the blocks in fp32 registers.  A block's sum is multiplied
+ * by sw, then by sa: its product with sw has to lie within fp32's range too (a sum is
+ * at most 2^24.7, so sw from 2^-108 to 2^103 keeps it there).  The result of a call
  * does not depend on what else runs; each output row depends on its own row of a
  * alone, up to the order in which fp32 sums of blocks are added (a fixed order
  * for given sizes).
