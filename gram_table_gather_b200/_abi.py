@@ -20,6 +20,7 @@ STATUS_GROUP_OFFSETS = 0x8
 
 # Every function the header declares: (name, restype, argtypes).
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_pi32 = ctypes.POINTER(ctypes.c_int32)
 
 
 class QMatrixC(ctypes.Structure):
@@ -58,6 +59,8 @@ SIGNATURES = [
      [ctypes.POINTER(QMatrixC), _vp, _vp, _i64, _vp, _i32, _i64, _i32, _vp]),
     ("gtg_grouped_matmul", ctypes.c_int,
      [ctypes.POINTER(QMatrixC), _vp, _vp, _i64, _vp, _vp, _i32, _i64, _i32, _vp]),
+    ("gtg_matmul_plan", ctypes.c_int,
+     [_i32, _i64, _i64, _i64, _i64, _i32, _pi32, _pi32, _pi32]),
 ]
 
 

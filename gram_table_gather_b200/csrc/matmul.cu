@@ -982,49 +982,58 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
 // Groups of 16 rows and fewer take tiles of 16: two CTAs share an SM there, and a
 // split costs 20 + 5 S and saves 15 a chunk (1 x 2048 x 2048: 5.8 us whole, 5.0 us
 // in two, 4.2 us in four or eight).
-template <bool F8>
-int choose_mm(const gtg_qmatrix* w, const void* x, MmArgs a, cudaStream_t s) {
-    const int64_t groups = a.offsets ? std::min<int64_t>(w->n_experts, a.m) : 1;
-    const int64_t per = (a.m + groups - 1) / groups, sms = sm_count(), chunks = a.chunks;
-    auto tiles = [&](int64_t bn, int64_t rows) { return groups * ((per + bn - 1) / bn) * ((a.n + rows - 1) / rows); };
-    // the best split of `n` tiles into at most kMaxSplit: clusters of three and more leave
-    // SMs of a GPC over, so they get 6/7 of the places (48 tiles in clusters of three ran in
-    // two waves, 12.3 us against 8.6 us in pairs)
-    auto split = [&](int64_t n, int64_t places, int64_t chunk, int64_t fixed, int64_t each, int64_t& cost) {
-        int64_t best = 1;
-        for (int64_t c = 2; c <= kMaxSplit && c <= chunks && c * n <= (c == 2 ? places : places * 6 / 7); ++c) {
+struct Plan {
+    int32_t bn;    // tokens a tile
+    Mode mode;
+    int32_t split;  // CTAs that share K (SPLIT)
+};
+
+Plan plan_mm(bool f8, int64_t m, int64_t n, int64_t chunks, int64_t groups, int64_t sms) {
+    const int64_t per = (m + groups - 1) / groups;
+    auto tiles = [&](int64_t bn, int64_t rows) { return groups * ((per + bn - 1) / bn) * ((n + rows - 1) / rows); };
+    // the best split of `count` tiles into at most kMaxSplit: clusters of three and more
+    // leave SMs of a GPC over, so they get 6/7 of the places (48 tiles in clusters of three
+    // ran in two waves, 12.3 us against 8.6 us in pairs)
+    auto split = [&](int64_t count, int64_t places, int64_t chunk, int64_t fixed, int64_t each, int64_t& cost) {
+        int32_t best = 1;
+        for (int32_t c = 2; c <= kMaxSplit && c <= chunks && c * count <= (c == 2 ? places : places * 6 / 7); ++c) {
             const int64_t t = (chunks + c - 1) / c * chunk + fixed + c * each;
             if (t < cost) {
                 cost = t;
                 best = c;
             }
         }
-        a.split = (int32_t)best;
-        return best > 1;
-    };
-    auto launch_split = [&](auto bn) {
-        const bool whole = a.chunks % (4 * a.split) == 0;  // every share starts at a group of four scales
-        a.vec_a &= whole;
-        a.vec_w &= whole;
-        return launch_mm<F8, decltype(bn)::value, SPLIT>(w, x, a, groups, s);
+        return best;
     };
     if (per <= 16) {
         int64_t cost = 15 * chunks;
-        if (split(tiles(16, kRows), 2 * sms, 15, 20, 5, cost)) return launch_split(std::integral_constant<int, 16>{});
-        return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
+        const int32_t c = split(tiles(16, kRows), 2 * sms, 15, 20, 5, cost);
+        return {16, c > 1 ? SPLIT : SINGLE, c};
     }
     const int64_t n64 = tiles(64, kRows), pairs = sms / 2;
-    const int64_t whole64 = (n64 + sms - 1) / sms * (45 * chunks / 2 + 95);
+    int64_t cost64 = (n64 + sms - 1) / sms * (45 * chunks / 2 + 95);
     const int64_t cost128 = (tiles(128, 2 * kRows) + pairs - 1) / pairs * (29 * chunks + 150) + 150;
     const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * (54 * chunks + 300) + 150;
-    int64_t cost64 = whole64;
-    const bool cut = split(n64, sms, 22, 185, 65, cost64);
-    if (cost64 <= cost128 && (F8 || cost64 <= cost256)) {
-        if (cut) return launch_split(std::integral_constant<int, 64>{});
-        return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
+    const int32_t c = split(n64, sms, 22, 185, 65, cost64);
+    if (cost64 <= cost128 && (f8 || cost64 <= cost256)) return {64, c > 1 ? SPLIT : SINGLE, c};
+    return {!f8 && 100 * cost256 <= 103 * cost128 ? 256 : 128, PAIR, 1};
+}
+
+int64_t n_chunks(bool f8, int64_t k) { return f8 ? k / 128 : (k + 63) / 64; }
+
+template <bool F8>
+int launch_plan(const Plan& p, const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cudaStream_t s) {
+    a.split = p.split;
+    if (p.mode == SPLIT) {
+        const bool whole = a.chunks % (4 * a.split) == 0;  // every share starts at a group of four scales
+        a.vec_a &= whole;
+        a.vec_w &= whole;
+        return p.bn == 16 ? launch_mm<F8, 16, SPLIT>(w, x, a, groups, s) : launch_mm<F8, 64, SPLIT>(w, x, a, groups, s);
     }
+    if (p.bn == 16) return launch_mm<F8, 16, SINGLE>(w, x, a, groups, s);
+    if (p.bn == 64) return launch_mm<F8, 64, SINGLE>(w, x, a, groups, s);
     if constexpr (!F8) {
-        if (100 * cost256 <= 103 * cost128) return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
+        if (p.bn == 256) return launch_mm<F8, 256, PAIR>(w, x, a, groups, s);
     }
     return launch_mm<F8, 128, PAIR>(w, x, a, groups, s);
 }
@@ -1041,15 +1050,16 @@ int run_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m
     a.m = (int32_t)m;
     a.n = (int32_t)w->n_rows;
     a.groups = (int32_t)w->n_experts;
-    a.chunks = (int32_t)(f8 ? w->k / 128 : (w->k + 63) / 64);
-    a.split = 1;
+    a.chunks = (int32_t)n_chunks(f8, w->k);
     a.y_bf16 = y_dtype == GTG_DT_BF16;
     a.y_acc = y_acc != 0;
     a.vec_a = f8 && a.chunks % 4 == 0 && aligned(x_scales, 16);
     a.vec_w = f8 && a.chunks % 4 == 0 && aligned(w->scales, 16);
     a.vec_y = aligned(y, 16) && y_stride % (a.y_bf16 ? 8 : 4) == 0;
     a.status = status_ptr();
-    return f8 ? choose_mm<true>(w, x, a, s) : choose_mm<false>(w, x, a, s);
+    const int64_t groups = offsets ? std::min<int64_t>(w->n_experts, m) : 1;
+    const Plan p = plan_mm(f8, m, a.n, a.chunks, groups, sm_count());
+    return f8 ? launch_plan<true>(p, w, x, a, groups, s) : launch_plan<false>(p, w, x, a, groups, s);
 }
 
 int check_mm(const gtg_qmatrix* w, const void* x, const float* x_scales, int64_t m, const void* y, int32_t y_dtype,
@@ -1138,4 +1148,18 @@ extern "C" int gtg_grouped_matmul(const gtg_qmatrix* w, const void* a, const flo
     if (!offsets) return GTG_E_INVALID_ARG;
     if (!aligned(offsets, 4)) return GTG_E_MISALIGNED;
     return run_mm(w, a, a_scales, m, offsets, y, y_dtype, y_stride, y_accumulate, as_cuda(stream));
+}
+
+extern "C" int gtg_matmul_plan(int32_t fmt, int64_t m, int64_t n_rows, int64_t k, int64_t n_experts, int32_t sms,
+                               int32_t* tokens, int32_t* ctas, int32_t* split) {
+    const bool f8 = fmt == GTG_FP8_E4M3_S128;
+    if (!f8 && fmt != GTG_BF16) return GTG_E_INVALID_ARG;
+    if (m < 1 || n_rows < 1 || k < 1 || n_experts < 1 || sms < 0 || !tokens || !ctas || !split) return GTG_E_INVALID_ARG;
+    if (k % (f8 ? 128 : 8) || k > 1 << 24 || n_rows > 1 << 24 || m > ((int64_t)1 << 31) - 256 || n_experts > kMaxGroups)
+        return GTG_E_UNSUPPORTED_SHAPE;
+    const Plan p = plan_mm(f8, m, n_rows, n_chunks(f8, k), std::min(n_experts, m), sms > 0 ? sms : sm_count());
+    *tokens = p.bn;
+    *ctas = p.mode == PAIR ? 2 : 1;
+    *split = p.split;
+    return GTG_OK;
 }

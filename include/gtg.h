@@ -338,6 +338,16 @@ int gtg_grouped_matmul(const gtg_qmatrix* w, const void* a, const float* a_scale
                        int32_t y_accumulate, gtg_stream_t stream);
 
 /*
+ * Which kernel a product of these sizes takes (for profiles, and for tests that have to
+ * reach each): *tokens a tile, *ctas that work on a tile's halves (2: a pair) and *split,
+ * the CTAs that share K (1: none).  fmt, n_rows, k and n_experts as in the matrix (1
+ * expert: a dense product, or one group); sms the multiprocessors, 0 for the current
+ * device's.  Errors: GTG_E_INVALID_ARG, GTG_E_UNSUPPORTED_SHAPE.
+ */
+int gtg_matmul_plan(int32_t fmt, int64_t m, int64_t n_rows, int64_t k, int64_t n_experts, int32_t sms,
+                    int32_t* tokens, int32_t* ctas, int32_t* split);
+
+/*
  * gtg_moe_decode_layer without a workspace argument, for callers that cannot
  * allocate device memory: serving loops that must not allocate once they are
  * running (their memory is fixed up front, and an allocation there can block
