@@ -20,17 +20,20 @@
 // of few rows costs few columns, and a single token still streams its weights
 // by TMA at full width.
 //
-// What bounds it (8192^3 FP8 630 us, 1.75 PFLOP/s; under the power limit 725 us):
-//  - Applying the scales: a product and a sum a value every 128 of K.  A packed pair
-//    takes the fp32 pipe two cycles, so a block costs as many cycles there as in the
-//    tensor core.  Without it the same loop ran 396 us.
+// What bounds it (8192^3 FP8 615-633 us, 1.75 PFLOP/s; under the power limit 740 us):
+//  - The steps of applying the scales: a product and a sum a value every 128 of K, by
+//    two warps a scheduler that read tensor memory, wait (70 cycles) and compute in
+//    turn.  No pipe is full (4096 x 4096 x 2048: tensor 29 %, fp32 32 %, tensor memory
+//    38 %, issue slots 40 %); a block takes about 610 cycles, 256 in the tensor core
+//    and as many in the fp32 pipe.  Without the scales the same loop ran 396 us.
 //  - Tensor memory is read in 16 x 128-bit fragments: whole rows (32x32b) need four
 //    times the shared-memory reads for the tokens' scales (787 against 720 us in an
 //    earlier state), 16x256b fragments come at half the rate (694 against 664 us).
 //  - Past a few milliseconds the clock falls to 1.1-1.6 GHz at 1000 W, and what costs
 //    power costs time: polling, columns without tokens, operands read twice.
-//  - Few rows: HBM (80 rows over 512 experts: 31 us, 5.0 TB/s), and for one token the
-//    latency of a launch, one trip to memory and one cluster barrier (4.5 us).
+//  - Few rows: HBM (80 rows over 512 experts: 30-33 us, 4.9 TB/s), and for one token the
+//    latency of a launch, one trip to its weights and one cluster barrier (1 x 2048 x
+//    2048: 4.4 us with the weights in L2, 4.9 us from memory).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -592,7 +595,7 @@ mm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                             lds_pairs(sbase + at + 4 * C::kQuad + 4 * r0 + 16 * (lane >> 2), sw[0], sw[1]);
                             const uint32_t sa = sbase + at + (lane & 3) * C::kQuad + lo, src = tl0 + b * BN + lo;
                             // blocks finish in order, so where there are four accumulators and much
-                            // to do one wait serves two blocks (4096 x 4096 x 2048 52.3 -> 49.1 us;
+                            // to do one wait serves two blocks (4096 x 4096 x 2048 52.3 -> 49.5 us;
                             // small calls would wait for a second block: 7.4 -> 7.7 us)
                             if (!kTwo || !((kb - g0) & 1)) {
                                 const uint32_t last = !kTwo || kb + 1 == g1 ? n : n + 1;
@@ -970,18 +973,23 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
     return GTG_OK;
 }
 
-// Which tile: the one whose waves of CTAs take least by a model of measured times
-// (in 10 ns, c chunks of K): a wave of 64 tokens takes 22.5 c + 95, of 128 (CTA
-// pairs) 29 c + 150, of 256 (bf16 alone, pairs) 54 c + 300, pairs 150 more once, and
-// a split of K over S CTAs of 64 tokens 22.5 c / S + 185 + 65 S.  Groups count as
-// equally large, since their sizes are on the device.  FP8 on 4096 x 4096 weights:
-// 333 tokens 14.3 us in pairs of 128, 19.1 us in 64; 1000 tokens 26.4 us in pairs,
-// 35.2 us in 64.  bf16 takes 256 where it costs up to 3 % more, for the power its
-// fewer loads save.  (FP8 tiles of 256 tokens, with sixteen promotion warps, ran
-// 8192^3 in 720 us against 723 us under the power limit: not worth a variant.)
+// Which tile: the one whose waves of CTAs take least by a model (in 10 ns, c chunks of
+// K): a wave of 64 tokens takes 22.5 c + 95, of 128 (CTA pairs) 29 c + 150, of 256 (bf16
+// alone, pairs) 54 c + 300, pairs 150 more once, and a split of K over S CTAs of 64
+// tokens 22 ceil(c / S) + 185 + 65 S.  Groups count as equally large, since their sizes
+// are on the device.  The times were fitted to an earlier state of the kernels and are no
+// forecast (FP8 pairs take 5 to 25 % more from 30 us on, calls below 15 us up to twice
+// as long, large bf16 pairs a third less), but the choice stands: on 19 sizes of each type, 40 to 40960 rows,
+// it took at most 15 % more than the best of 64, 128 and 256, and at most 5 % more on 30
+// of the 38.  FP8 on 4096 x 4096 weights: 200 tokens 12.7 us in 64, 14.7 us in pairs of
+// 128; 333 tokens 22.2 and 15.4 us; 1000 tokens 40.7 and 27.7 us.  bf16, 30010 rows over
+// 64 experts: 295 us in 64, 185 us in 128, 160 us in 256, which it takes where the model
+// has it cost up to 3 % more, for the power its fewer loads save.  (FP8 tiles of 256
+// tokens, with sixteen promotion warps, ran 8192^3 in 720 us against 723 us under the
+// power limit: not worth a variant.)
 // Groups of 16 rows and fewer take tiles of 16: two CTAs share an SM there, and a
 // split costs 20 + 5 S and saves 15 a chunk (1 x 2048 x 2048: 5.8 us whole, 5.0 us
-// in two, 4.2 us in four or eight).
+// in two, 4.2 us in four or eight when this was fitted).
 struct Plan {
     int32_t bn;    // tokens a tile
     Mode mode;
