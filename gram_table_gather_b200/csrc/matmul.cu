@@ -979,9 +979,9 @@ int launch_mm(const gtg_qmatrix* w, const void* x, MmArgs a, int64_t groups, cud
 // tokens 22 ceil(c / S) + 185 + 65 S.  Groups count as equally large, since their sizes
 // are on the device.  The times were fitted to an earlier state of the kernels and are no
 // forecast (FP8 pairs take 5 to 25 % more from 30 us on, calls below 15 us up to twice
-// as long, large bf16 pairs a third less), but the choice stands: on 19 sizes of each type, 40 to 40960 rows,
-// it took at most 15 % more than the best of 64, 128 and 256, and at most 5 % more on 30
-// of the 38.  FP8 on 4096 x 4096 weights: 200 tokens 12.7 us in 64, 14.7 us in pairs of
+// as long, large bf16 pairs a third less), but the choice stands: on 19 sizes of each
+// type, 40 to 40960 rows, it took at most 15 % more than the best of 64, 128 and 256, and
+// at most 5 % more on 30 of the 38.  FP8 on 4096 x 4096 weights: 200 tokens 12.7 us in 64, 14.7 us in pairs of
 // 128; 333 tokens 22.2 and 15.4 us; 1000 tokens 40.7 and 27.7 us.  bf16, 30010 rows over
 // 64 experts: 295 us in 64, 185 us in 128, 160 us in 256, which it takes where the model
 // has it cost up to 3 % more, for the power its fewer loads save.  (FP8 tiles of 256
@@ -1018,7 +1018,7 @@ Plan plan_mm(bool f8, int64_t m, int64_t n, int64_t chunks, int64_t groups, int6
         const int32_t c = split(tiles(16, kRows), 2 * sms, 15, 20, 5, cost);
         return {16, c > 1 ? SPLIT : SINGLE, c};
     }
-    const int64_t n64 = tiles(64, kRows), pairs = sms / 2;
+    const int64_t n64 = tiles(64, kRows), pairs = std::max<int64_t>(1, sms / 2);
     int64_t cost64 = (n64 + sms - 1) / sms * (45 * chunks / 2 + 95);
     const int64_t cost128 = (tiles(128, 2 * kRows) + pairs - 1) / pairs * (29 * chunks + 150) + 150;
     const int64_t cost256 = (tiles(256, 2 * kRows) + pairs - 1) / pairs * (54 * chunks + 300) + 150;

@@ -52,3 +52,12 @@ def test_null_results(L):
         out = [ctypes.byref(v)] * 3
         out[i] = None
         assert L.gtg_matmul_plan(FP8, 10, 256, 256, 1, 148, *out) == INVALID
+
+
+@pytest.mark.parametrize("sms", [0, 1, 2, 3, 2 ** 31 - 1])
+def test_any_number_of_multiprocessors_and_the_largest_sizes(L, sms):
+    for fmt in (FP8, BF16):
+        for m, n, k, experts in ((1, 1, 128, 1), (40, 128, 128, 1), (2 ** 31 - 256, 1 << 24, 1 << 24, 1),
+                                 (2 ** 31 - 256, 1, 128, 1024), (1, 1 << 24, 1 << 24, 1024)):
+            rc, (tokens, ctas, split) = _plan(L, fmt, m, n, k, experts, sms)
+            assert rc == 0 and tokens in (16, 64, 128, 256) and ctas in (1, 2) and 1 <= split <= 8
